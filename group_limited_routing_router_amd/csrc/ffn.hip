@@ -27,34 +27,14 @@
 // is an upper bound, every workgroup rebuilds the per-expert tile prefix sum
 // from expert_offsets in LDS and maps itself to a tile, and surplus
 // workgroups exit.  The mapping is XCD-aware (see find_tile).
-#include <type_traits>
-
 #include "common.h"
 #include "kernels.h"
+#include "tiles.h"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / kWave;
-constexpr int kMaxE = 256;
 constexpr int BK = 64;           // K elements per LDS stage (large-tile kernel)
-
-// Raw buffer resource over [base, base + bytes): 32-bit offsets from one
-// scalar base; loads past `bytes` return zero.  Third dword: gfx9 default.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), static_cast<short>(0),
-                                             static_cast<int>(bytes), 0x00020000);
-}
-
-// Compile-time loop: f(std::integral_constant<int, I>) for I in [B, E).
-template <int B, int E, typename F>
-__device__ __forceinline__ void static_for(F&& f) {
-    if constexpr (B < E) {
-        f(std::integral_constant<int, B>{});
-        static_for<B + 1, E>(f);
-    }
-}
 
 struct FfnArgs {
     int64_t P;       // pairs (rows of h and y)
@@ -75,92 +55,6 @@ struct FfnArgs {
     bool stream_w = false;   // small tiles: every weight is read once (about one row
                              // tile per expert), so it streams past the caches
 };
-
-// Map this workgroup to a tile (expert e, column tile nt, row range
-// [row0, row0 + rows)).  Every workgroup rebuilds the prefix sum of per-expert
-// row tiles from expert_offsets in LDS (no host read-back); an expert with n
-// rows gets ceil(n / BM) row tiles.  The tile list is ordered
-// by expert position, then column tile, then row tile; workgroup b runs on
-// XCD b % 8 and XCD x takes the x-th contiguous run of the list, so the row
-// tiles that share a weight tile are neighbours on one XCD.  Expert positions
-// interleave the experts (position i holds expert (i % 8) * (E / 8) + i / 8
-// when 8 divides E), so each XCD's run draws on every group of consecutive
-// experts and a few heavily routed neighbours do not land on one XCD.
-// GRAN = 1 splits an expert's rows evenly over its row tiles; GRAN > 1 gives
-// every row tile but the last the same multiple of GRAN rows (for the large
-// tile, whose two row waves take alternate 32-row blocks: 64-row multiples
-// keep them equally busy).  Returns false for surplus workgroups (uniform
-// over the workgroup).  s_off holds kMaxE + 1 entries, s_tstart
-// kMaxE + 1 + kWaves.
-template <int BM, int GRAN = 1>
-__device__ bool find_tile(const FfnArgs& a, int ncol_tiles, int32_t* s_off, int32_t* s_tstart,
-                          int& e_out, int& nt_out, int& row0_out, int& rows_out) {
-    const int tid = threadIdx.x;
-    const int E = a.E;
-    for (int e = tid; e <= E; e += kThreads) {
-        int64_t o = a.offsets[e];
-        o = o < 0 ? 0 : (o > a.P ? a.P : o);
-        s_off[e] = static_cast<int32_t>(o);
-    }
-    __syncthreads();
-    // expert at list position i
-    const bool interleave = E % kNumXcd == 0;
-    auto expert_at = [&](int i) { return interleave ? (i % kNumXcd) * (E / kNumXcd) + i / kNumXcd : i; };
-    int cnt = 0;
-    if (tid < E) {
-        const int ex = expert_at(tid);
-        const int n = s_off[ex + 1] - s_off[ex];
-        cnt = n > 0 ? (n + BM - 1) / BM : 0;
-    }
-    // inclusive prefix sum over positions (kThreads == kMaxE): within each
-    // wave by shuffles, then the totals of the waves before it
-    const int lane = tid & (kWave - 1), wave = tid / kWave;
-    int incl = cnt;
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-        const int v = __shfl_up(incl, d, kWave);
-        if (lane >= d) incl += v;
-    }
-    int32_t* s_wave_total = s_tstart + (kMaxE + 1);
-    if (lane == kWave - 1) s_wave_total[wave] = incl;
-    __syncthreads();
-    for (int w = 0; w < wave; ++w) incl += s_wave_total[w];
-    s_tstart[tid + 1] = incl;  // exclusive prefix over positions; s_tstart[E] = total row tiles
-    if (tid == 0) s_tstart[0] = 0;
-    __syncthreads();
-    const int64_t total = static_cast<int64_t>(s_tstart[E]) * ncol_tiles;
-    const int xcd = blockIdx.x % kNumXcd;
-    const int64_t local = blockIdx.x / kNumXcd;
-    const int64_t per = total / kNumXcd, rem = total % kNumXcd;
-    if (local >= per + (xcd < rem ? 1 : 0)) return false;
-    const int64_t L = xcd * per + (xcd < rem ? xcd : rem) + local;
-    int lo = 0, hi = E - 1;  // last position i with s_tstart[i] * ncol_tiles <= L
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (static_cast<int64_t>(s_tstart[mid]) * ncol_tiles <= L) lo = mid; else hi = mid - 1;
-    }
-    const int pos = lo;
-    const int e = expert_at(pos);
-    const int tiles_e = s_tstart[pos + 1] - s_tstart[pos];  // >= 1 for the position found
-    const int64_t rel = L - static_cast<int64_t>(s_tstart[pos]) * ncol_tiles;
-    const int nt = static_cast<int>(rel / tiles_e);
-    const int mt = static_cast<int>(rel - static_cast<int64_t>(nt) * tiles_e);
-    const int n_e = s_off[e + 1] - s_off[e];
-    e_out = e;
-    nt_out = nt;
-    if constexpr (GRAN == 1) {
-        const int base = n_e / tiles_e, extra = n_e % tiles_e;
-        row0_out = s_off[e] + mt * base + (mt < extra ? mt : extra);
-        rows_out = base + (mt < extra ? 1 : 0);
-    } else {
-        // per <= BM since GRAN divides BM, so the last tile keeps >= 1 row
-        static_assert(BM % GRAN == 0, "granule divides the tile");
-        const int per = ((n_e + tiles_e - 1) / tiles_e + GRAN - 1) / GRAN * GRAN;
-        row0_out = s_off[e] + mt * per;
-        rows_out = min(per, n_e - mt * per);
-    }
-    return true;
-}
 
 // FP8 E4M3 codes -> bf16, eight at a time, two per instruction.  With a unit
 // scale the gfx950 conversion is exact (OCP e4m3fn codes; every E4M3 value is
@@ -217,7 +111,7 @@ __global__ __launch_bounds__(kThreads) void ffn_gemm_kernel(FfnArgs a) {
     const int wave = tid >> 6;
 
     int e, nt, row0, rows;
-    if (!find_tile<BM>(a, a.N / BN_OUT, s_off, s_tstart, e, nt, row0, rows)) return;
+    if (!find_tile<BM>(a.offsets, a.P, a.E, a.N / BN_OUT, s_off, s_tstart, e, nt, row0, rows)) return;
     const int n0 = nt * BN_OUT;
     const int K = a.K;
 
@@ -402,13 +296,6 @@ hipError_t launch_gemm(const FfnArgs& a, hipStream_t s) {
     return launch_gemm_nt<BM, BN, WAVES_M, WAVES_N, GATEUP, FP8, SK, false>(a, s);
 }
 
-// The large tile reads its operands through buffer resources with 32-bit
-// offsets.  A stage row past the tile's last 32-row block gets this offset,
-// which lies past the end of any operand the kernel takes (x of at most
-// kNoRowOffset bytes, so up to 4 GiB less 1 MiB) and cannot wrap when a
-// stage's K offset is added, so its loads fetch nothing.
-constexpr uint32_t kNoRowOffset = 0xFFF00000u;
-
 // Large-tile GEMM for experts with many rows (prefill and longer).
 //
 // 32x32x16 MFMA; a 256-thread workgroup owns a 256 x 256 tile and each of its
@@ -429,24 +316,6 @@ constexpr uint32_t kNoRowOffset = 0xFFF00000u;
 // (vmcnt) before each barrier, and for all of them before it ends.  Results
 // are stored straight from the accumulators (see the epilogue).
 constexpr int kDmaArena = 163840;  // the whole LDS of a gfx950 workgroup
-
-__device__ __forceinline__ void dma_load16(uint32_t lds_byte_addr, __amdgpu_buffer_rsrc_t rsrc,
-                                           uint32_t voffset, uint32_t soffset) {
-    asm volatile(
-        "s_mov_b32 m0, %0\n\t"
-        "s_nop 0\n\t"
-        "buffer_load_dwordx4 %1, %2, %3 offen lds"
-        :
-        : "s"(__builtin_amdgcn_readfirstlane(lds_byte_addr)), "v"(voffset), "s"(rsrc),
-          "s"(__builtin_amdgcn_readfirstlane(soffset))
-        : "memory", "m0");
-}
-
-template <int N>
-__device__ __forceinline__ void wait_vmcnt() {
-    static_assert(N >= 0 && N < 64, "vmcnt range");
-    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
-}
 
 // FP8 = true: the weights are E4M3 codes, widened to bf16 as each MFMA
 // operand is read; the per-channel scale multiplies the accumulators before
@@ -490,7 +359,7 @@ __global__ __launch_bounds__(kThreads) void ffn_gemm_dma_kernel(FfnArgs a) {
     {
         int32_t* s_off = reinterpret_cast<int32_t*>(s_arena);
         int32_t* s_tstart = s_off + (kMaxE + 1);
-        if (!find_tile<BM, 32 * WAVES_M>(a, a.N / BN_OUT, s_off, s_tstart, e, nt, row0, rows)) return;
+        if (!find_tile<BM, 32 * WAVES_M>(a.offsets, a.P, a.E, a.N / BN_OUT, s_off, s_tstart, e, nt, row0, rows)) return;
         __syncthreads();  // everyone is done with the schedule before DMA reuses the arena
     }
     const int n0 = nt * BN_OUT;

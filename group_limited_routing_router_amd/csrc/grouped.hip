@@ -1,0 +1,228 @@
+// grouped.hip -- the experts' matrix products by themselves: the product, its
+// two gradients, and the product in 8-bit integers, grouped by expert over
+// the sorted positions.
+//
+//   product      out[q,n]  = sum_k a[row(q),k] w[e,n,k]
+//   input grad   da[q,k]   = sum_n dout[q,n] w[e,n,k]
+//   weight grad  dw[e,n,k] = sum_{q of e} dout[q,n] a[row(q),k]
+//   int8         out[q,n]  = a_scale[row(q)] w_scale[e,n] sum_k a[row(q),k] w[e,n,k]
+#include "common.h"
+#include "kernels.h"
+#include "tiles.h"
+
+namespace moe {
+namespace {
+
+enum Mode { kProduct = 0, kInputGrad = 1, kWeightGrad = 2 };
+
+// The rows of the sorted order that expert e owns, clamped to [0, P].
+__device__ __forceinline__ void expert_rows(const GemmArgs& g, int e, int64_t& first, int64_t& n) {
+    int64_t b = 0, t = g.P;
+    if (g.offsets) {
+        b = g.offsets[e];
+        t = g.offsets[e + 1];
+        b = b < 0 ? 0 : (b > g.P ? g.P : b);
+        t = t < 0 ? 0 : (t > g.P ? g.P : t);
+    }
+    first = b;
+    n = t > b ? t - b : 0;
+}
+
+// Activation row of sorted position q, clamped to [0, S).
+__device__ __forceinline__ int64_t source_row(const GemmArgs& g, int64_t q) {
+    if (!g.pairs) return q;
+    int64_t r = g.pairs[q] / g.k;
+    return r < 0 ? 0 : (r >= g.S ? g.S - 1 : r);
+}
+
+// The plain kernel: one 64 x 64 tile of the output, the reduction in steps of
+// 64 bytes a row through LDS.  In LDS both operands lie with the reduction
+// along the row; an operand whose reduction runs down the rows in memory is
+// transposed on the way in.  Grid: (column tiles, row tiles of the fullest
+// possible expert or, for the weight gradient, row tiles of N, experts).
+template <int MODE, bool I8>
+__global__ __launch_bounds__(kThreads) void gemm_plain_kernel(GemmArgs g) {
+    constexpr int EB = I8 ? 1 : 2;        // bytes per operand element
+    constexpr int PER16 = 16 / EB;        // elements per 16 bytes
+    constexpr int BK = 64 / EB;           // reduction per step
+    constexpr int PITCH = 64 + 16;        // bytes per LDS row
+    __shared__ __attribute__((aligned(16))) unsigned char s_y[64 * PITCH];  // output rows
+    __shared__ __attribute__((aligned(16))) unsigned char s_x[64 * PITCH];  // output columns
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int e = blockIdx.z;
+    int64_t first, n_e;
+    expert_rows(g, e, first, n_e);
+    // output: rows [r0, rows) x columns [c0, cols); reduction over [0, red)
+    const int64_t rows = MODE == kWeightGrad ? g.N : n_e;
+    const int cols = MODE == kProduct ? g.N : g.K;
+    const int64_t red = MODE == kProduct ? g.K : (MODE == kInputGrad ? g.N : n_e);
+    const int c0 = blockIdx.x * 64;
+    const unsigned char* a = static_cast<const unsigned char*>(g.a);
+    const unsigned char* w = static_cast<const unsigned char*>(g.w) +
+                             static_cast<int64_t>(e) * g.N * g.K * EB;
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.y) * 64; r0 < rows;
+         r0 += static_cast<int64_t>(gridDim.y) * 64) {
+        f32x4 acc[4];
+        i32x4 iacc[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+            iacc[c] = i32x4{0, 0, 0, 0};
+        }
+        for (int64_t k0 = 0; k0 < red; k0 += BK) {
+            const u32x4 zero = {0, 0, 0, 0};
+            // one 16-byte piece of each operand a thread
+            {
+                u32x4 v = zero;
+                if constexpr (MODE == kWeightGrad) {  // dout[q, n..n+7]: transposed
+                    const int kk = tid >> 3, rr = (tid & 7) * 8;
+                    if (k0 + kk < red && r0 + rr < rows)
+                        v = ld16(static_cast<const unsigned char*>(g.dout) +
+                                 ((first + k0 + kk) * g.N + r0 + rr) * EB);
+                    const uint16_t* h = reinterpret_cast<const uint16_t*>(&v);
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint16_t*>(&s_y[(rr + i) * PITCH + kk * 2]) = h[i];
+                } else {
+                    const int rr = tid >> 2, kk = (tid & 3) * PER16;
+                    if (r0 + rr < rows && k0 + kk < red) {
+                        const int64_t q = first + r0 + rr;
+                        v = MODE == kProduct
+                                ? ld16(a + (source_row(g, q) * g.K + k0 + kk) * EB)
+                                : ld16(static_cast<const unsigned char*>(g.dout) + (q * g.N + k0 + kk) * EB);
+                    }
+                    *reinterpret_cast<u32x4*>(&s_y[rr * PITCH + (tid & 3) * 16]) = v;
+                }
+            }
+            {
+                u32x4 v = zero;
+                if constexpr (MODE == kProduct) {
+                    const int cc = tid >> 2, kk = (tid & 3) * PER16;
+                    if (c0 + cc < cols && k0 + kk < red)
+                        v = ld16(w + (static_cast<int64_t>(c0 + cc) * g.K + k0 + kk) * EB);
+                    *reinterpret_cast<u32x4*>(&s_x[cc * PITCH + (tid & 3) * 16]) = v;
+                } else {
+                    const int kk = tid >> 3, cc = (tid & 7) * 8;
+                    if (k0 + kk < red && c0 + cc < cols)
+                        v = MODE == kInputGrad
+                                ? ld16(w + ((k0 + kk) * g.K + c0 + cc) * EB)
+                                : ld16(a + (source_row(g, first + k0 + kk) * g.K + c0 + cc) * EB);
+                    const uint16_t* h = reinterpret_cast<const uint16_t*>(&v);
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint16_t*>(&s_x[(cc + i) * PITCH + kk * 2]) = h[i];
+                }
+            }
+            __syncthreads();
+            const u32x4 yv = ld16(&s_y[(wave * 16 + (lane & 15)) * PITCH + (lane >> 4) * 16]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const u32x4 xv = ld16(&s_x[(c * 16 + (lane & 15)) * PITCH + (lane >> 4) * 16]);
+                if constexpr (I8)
+                    iacc[c] = mfma16_i8(yv, xv, iacc[c]);
+                else
+                    acc[c] = mfma16(as_bf16x8(yv), as_bf16x8(xv), acc[c]);
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t r = r0 + wave * 16 + 4 * (lane >> 4) + i;
+                const int col = c0 + c * 16 + (lane & 15);
+                if (r >= rows || col >= cols) continue;
+                float v = acc[c][i];
+                if constexpr (I8)
+                    v = static_cast<float>(iacc[c][i]) *
+                        (g.a_scale[source_row(g, first + r)] *
+                         g.w_scale[static_cast<int64_t>(e) * g.N + col]);
+                const int64_t at = MODE == kWeightGrad
+                                       ? (static_cast<int64_t>(e) * g.N + r) * g.K + col
+                                       : (first + r) * cols + col;
+                if (g.out_bf16)
+                    static_cast<uint16_t*>(g.out)[at] = f32_to_bf16_rne(v);
+                else if (g.accumulate)
+                    static_cast<float*>(g.out)[at] += v;
+                else
+                    static_cast<float*>(g.out)[at] = v;
+            }
+    }
+}
+
+template <int MODE, bool I8>
+hipError_t launch_plain(const GemmArgs& g, hipStream_t s) {
+    const int cols = MODE == kProduct ? g.N : g.K;
+    const int64_t rows = MODE == kWeightGrad ? g.N : g.P;
+    if (rows <= 0) return hipSuccess;
+    const int64_t rt = (rows + 63) / 64;
+    const dim3 grid((cols + 63) / 64, static_cast<unsigned>(rt < 1024 ? rt : 1024), g.E);
+    gemm_plain_kernel<MODE, I8><<<grid, dim3(kThreads), 0, s>>>(g);
+    return hipGetLastError();
+}
+
+// One row of bf16 per workgroup: its largest magnitude, then its codes.
+__global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const uint16_t* x, int K, int8_t* codes,
+                                                                 float* scales) {
+    __shared__ float s_max[kWaves];
+    __shared__ int s_bad[kWaves];
+    const int64_t r = blockIdx.x;
+    const int tid = threadIdx.x;
+    const uint16_t* row = x + r * K;
+    float m = 0.0f;
+    int bad = 0;
+    for (int c = tid * 8; c < K; c += kThreads * 8) {
+        const u32x4 v = ld16(row + c);
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(&v);
+        for (int i = 0; i < 8; ++i) {
+            m = fmaxf(m, fabsf(bf16_to_f32(h[i])));
+            bad |= (h[i] & 0x7f80) == 0x7f80;
+        }
+    }
+    for (int d = 32; d; d >>= 1) {
+        m = fmaxf(m, __shfl_xor(m, d, kWave));
+        bad |= __shfl_xor(bad, d, kWave);
+    }
+    if ((tid & 63) == 0) {
+        s_max[tid >> 6] = m;
+        s_bad[tid >> 6] = bad;
+    }
+    __syncthreads();
+    for (int w = 0; w < kWaves; ++w) {
+        m = fmaxf(m, s_max[w]);
+        bad |= s_bad[w];
+    }
+    const bool zero = bad || m < 0x1p-100f;
+    // 127 x is exact in fp32 (15 bits) and the division correctly rounded, so
+    // a quotient half way between two codes is met exactly (x = amax / 2 is
+    // one); large rows are scaled down first, since 127 x would overflow
+    const float shrink = m > 0x1p100f ? 0x1p-30f : 1.0f;
+    if (tid == 0) scales[r] = bad ? __builtin_nanf("") : (zero ? 1.0f : m / 127.0f);
+    for (int c = tid * 8; c < K; c += kThreads * 8) {
+        const u32x4 v = ld16(row + c);
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(&v);
+        union { int8_t b[8]; uint64_t u; } o;
+        for (int i = 0; i < 8; ++i)
+            o.b[i] = zero ? 0 : static_cast<int8_t>(rintf(bf16_to_f32(h[i]) * shrink * 127.0f / (m * shrink)));
+        *reinterpret_cast<uint64_t*>(codes + r * K + c) = o.u;
+    }
+}
+
+}  // namespace
+
+size_t grouped_ws_bytes(const GemmArgs&) { return 0; }
+
+hipError_t launch_grouped_gemm(const GemmArgs& g, hipStream_t s) { return launch_plain<kProduct, false>(g, s); }
+
+hipError_t launch_grouped_dgrad(const GemmArgs& g, hipStream_t s) { return launch_plain<kInputGrad, false>(g, s); }
+
+hipError_t launch_grouped_wgrad(const GemmArgs& g, hipStream_t s) { return launch_plain<kWeightGrad, false>(g, s); }
+
+hipError_t launch_grouped_int8(const GemmArgs& g, hipStream_t s) { return launch_plain<kProduct, true>(g, s); }
+
+hipError_t launch_quantize_rows(int64_t rows, int K, const uint16_t* x, int8_t* codes, float* scales,
+                                hipStream_t s) {
+    if (rows <= 0) return hipSuccess;
+    quantize_rows_kernel<<<dim3(static_cast<unsigned>(rows)), dim3(kThreads), 0, s>>>(x, K, codes, scales);
+    return hipGetLastError();
+}
+
+}  // namespace moe

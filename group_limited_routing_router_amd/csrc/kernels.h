@@ -12,6 +12,25 @@ struct Problem {
     float scale;
 };
 
+// A grouped product (moe_gemm.h): shape, operands, output.
+struct GemmArgs {
+    int64_t P;               // sorted positions
+    int64_t S;               // rows of a
+    int E, N, K;             // w is [E,N,K]
+    int k;                   // row(q) = pairs[q] / k
+    const void* a;           // activations [S,K]: bf16 or int8 codes
+    const void* dout;        // output gradient [P,N] bf16 (the two gradients)
+    const void* w;           // weights [E,N,K]: bf16 or int8 codes
+    const int32_t* pairs;    // [P], or NULL: row(q) = q
+    const int32_t* offsets;  // [E+1], or NULL (E = 1): all P rows
+    const float* a_scale;    // int8: [S]
+    const float* w_scale;    // int8: [E,N]
+    void* out;
+    bool out_bf16;           // out is bf16, else fp32
+    bool accumulate;         // out += (fp32)
+    void* ws;
+};
+
 // Pairs handled by one block of the counting sort.
 constexpr int kPermuteChunk = 4096;
 
@@ -71,5 +90,17 @@ constexpr int kResidualMaxH = kResidualMaxChunks * 4 * 256;
 hipError_t launch_combine_residual(const Problem& p, const float* y, const int32_t* pair_rows,
                                    const float* weights, const float* gain, float eps,
                                    float wa, float wb, float* res, hipStream_t s);
+
+// Scratch the grouped products of this shape need.
+size_t grouped_ws_bytes(const GemmArgs& g);
+
+hipError_t launch_grouped_gemm(const GemmArgs& g, hipStream_t s);
+hipError_t launch_grouped_dgrad(const GemmArgs& g, hipStream_t s);
+hipError_t launch_grouped_wgrad(const GemmArgs& g, hipStream_t s);
+hipError_t launch_grouped_int8(const GemmArgs& g, hipStream_t s);
+
+// Rows of bf16 [rows,K] as int8 codes with one fp32 scale each.
+hipError_t launch_quantize_rows(int64_t rows, int K, const uint16_t* x, int8_t* codes, float* scales,
+                                hipStream_t s);
 
 }  // namespace moe

@@ -11,6 +11,7 @@
 #include <string>
 
 #include "moe.h"
+#include "moe_gemm.h"
 #include "kernels.h"
 
 #define MOE_EXPORT extern "C" __attribute__((visibility("default")))
@@ -467,6 +468,199 @@ MOE_EXPORT moe_status moe_forward_noalloc(const moe_problem* p, const moe_bf16* 
     // it is read), so the previous call's contents need no clearing
     return moe_forward(p, x, w_router, bias, w_gate, w_up, w_down, out, out_dtype, topk_ids,
                        topk_weights, y, ws, need, stream);
+}
+
+// ---- grouped products (moe_gemm.h) ----
+
+namespace {
+
+moe_status check_gemm(const moe_gemm_problem* g, int multiple) {
+    if (!g) return fail(MOE_ERR_INVALID_ARG, "problem is NULL");
+    if (g->P < 0 || g->P > 0x7fffffffLL)
+        return fail(MOE_ERR_INVALID_ARG, "P=%lld must be in [0, 2^31)", (long long)g->P);
+    if (g->S < 0 || g->S > 0x7fffffffLL)
+        return fail(MOE_ERR_INVALID_ARG, "S=%lld must be in [0, 2^31)", (long long)g->S);
+    if (g->E <= 0) return fail(MOE_ERR_INVALID_ARG, "E=%d must be positive", g->E);
+    if (g->k < 1) return fail(MOE_ERR_INVALID_ARG, "k=%d must be positive", g->k);
+    if (g->N <= 0 || g->N % multiple != 0)
+        return fail(MOE_ERR_INVALID_ARG, "N=%d must be a positive multiple of %d", g->N, multiple);
+    if (g->K <= 0 || g->K % multiple != 0)
+        return fail(MOE_ERR_INVALID_ARG, "K=%d must be a positive multiple of %d", g->K, multiple);
+    if (g->E > 256) return fail(MOE_ERR_UNSUPPORTED, "E=%d > 256", g->E);
+    if (g->N > kMaxDim) return fail(MOE_ERR_UNSUPPORTED, "N=%d > %d", g->N, kMaxDim);
+    if (g->K > kMaxDim) return fail(MOE_ERR_UNSUPPORTED, "K=%d > %d", g->K, kMaxDim);
+    return MOE_OK;
+}
+
+// The rows the positions read: every position is its own row without pairs.
+moe_status check_rows(const moe_gemm_problem& g, const int32_t* sorted_pairs) {
+    if (!sorted_pairs && g.S < g.P)
+        return fail(MOE_ERR_INVALID_ARG, "S=%lld rows for P=%lld positions without sorted_pairs",
+                    (long long)g.S, (long long)g.P);
+    if (sorted_pairs && g.P > 0 && g.S < 1)
+        return fail(MOE_ERR_INVALID_ARG, "S=%lld rows for P=%lld positions", (long long)g.S, (long long)g.P);
+    return check_ptr(sorted_pairs, "sorted_pairs", true);
+}
+
+moe_status check_offsets(const moe_gemm_problem& g, const int32_t* expert_offsets) {
+    return check_ptr(expert_offsets, "expert_offsets", g.E == 1);
+}
+
+moe_status check_gemm_out(moe_dtype dtype, int accumulate) {
+    if (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16)
+        return fail(MOE_ERR_INVALID_ARG, "dtype=%d is not MOE_DTYPE_F32/BF16", (int)dtype);
+    if (accumulate && dtype != MOE_DTYPE_F32)
+        return fail(MOE_ERR_INVALID_ARG, "accumulate needs an fp32 output");
+    return MOE_OK;
+}
+
+moe::GemmArgs gemm_args(const moe_gemm_problem& g) {
+    moe::GemmArgs a{};
+    a.P = g.P;
+    a.S = g.S;
+    a.E = g.E;
+    a.N = g.N;
+    a.K = g.K;
+    a.k = g.k;
+    return a;
+}
+
+size_t gemm_ws_bytes(const moe_gemm_problem& g) {
+    return moe::grouped_ws_bytes(gemm_args(g));
+}
+
+moe_status check_gemm_ws(const moe_gemm_problem& g, const void* ws, size_t ws_bytes) {
+    const size_t need = gemm_ws_bytes(g);
+    if (need == 0) return MOE_OK;
+    if (!ws) return fail(MOE_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", need);
+    if (reinterpret_cast<uintptr_t>(ws) % 16 != 0)
+        return fail(MOE_ERR_WORKSPACE, "workspace is not 16-byte aligned");
+    if (ws_bytes < need)
+        return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, need %zu", ws_bytes, need);
+    return MOE_OK;
+}
+
+}  // namespace
+
+MOE_EXPORT size_t moe_gemm_workspace_bytes(const moe_gemm_problem* g) {
+    if (check_gemm(g, 8) != MOE_OK) return 0;
+    ok();
+    return gemm_ws_bytes(*g);
+}
+
+MOE_EXPORT moe_status moe_grouped_gemm(const moe_gemm_problem* g, const moe_bf16* a,
+                                       const int32_t* sorted_pairs, const int32_t* expert_offsets,
+                                       const moe_bf16* w, void* out, moe_dtype out_dtype, void* ws,
+                                       size_t ws_bytes, hipStream_t stream) {
+    MOE_TRY(check_gemm(g, 8));
+    MOE_TRY(check_gemm_out(out_dtype, 0));
+    MOE_TRY(check_rows(*g, sorted_pairs));
+    if (g->P == 0) return ok();
+    MOE_TRY(check_offsets(*g, expert_offsets));
+    MOE_TRY(check_ptr(a, "a"));
+    MOE_TRY(check_ptr(w, "w"));
+    MOE_TRY(check_ptr(out, "out"));
+    MOE_TRY(check_gemm_ws(*g, ws, ws_bytes));
+    moe::GemmArgs x = gemm_args(*g);
+    x.a = a;
+    x.w = w;
+    x.pairs = sorted_pairs;
+    x.offsets = expert_offsets;
+    x.out = out;
+    x.out_bf16 = out_dtype == MOE_DTYPE_BF16;
+    x.ws = ws;
+    return hip_status(moe::launch_grouped_gemm(x, stream), "grouped gemm launch");
+}
+
+MOE_EXPORT moe_status moe_grouped_gemm_dgrad(const moe_gemm_problem* g, const moe_bf16* dout,
+                                             const int32_t* expert_offsets, const moe_bf16* w,
+                                             void* da, moe_dtype da_dtype, int accumulate, void* ws,
+                                             size_t ws_bytes, hipStream_t stream) {
+    MOE_TRY(check_gemm(g, 8));
+    MOE_TRY(check_gemm_out(da_dtype, accumulate));
+    if (g->P == 0) return ok();
+    MOE_TRY(check_offsets(*g, expert_offsets));
+    MOE_TRY(check_ptr(dout, "dout"));
+    MOE_TRY(check_ptr(w, "w"));
+    MOE_TRY(check_ptr(da, "da"));
+    MOE_TRY(check_gemm_ws(*g, ws, ws_bytes));
+    moe::GemmArgs x = gemm_args(*g);
+    x.dout = dout;
+    x.w = w;
+    x.offsets = expert_offsets;
+    x.out = da;
+    x.out_bf16 = da_dtype == MOE_DTYPE_BF16;
+    x.accumulate = accumulate != 0;
+    x.ws = ws;
+    return hip_status(moe::launch_grouped_dgrad(x, stream), "grouped gemm input gradient launch");
+}
+
+MOE_EXPORT moe_status moe_grouped_gemm_wgrad(const moe_gemm_problem* g, const moe_bf16* dout,
+                                             const moe_bf16* a, const int32_t* sorted_pairs,
+                                             const int32_t* expert_offsets, void* dw,
+                                             moe_dtype dw_dtype, int accumulate, void* ws,
+                                             size_t ws_bytes, hipStream_t stream) {
+    MOE_TRY(check_gemm(g, 8));
+    MOE_TRY(check_gemm_out(dw_dtype, accumulate));
+    MOE_TRY(check_rows(*g, sorted_pairs));
+    MOE_TRY(check_offsets(*g, expert_offsets));
+    MOE_TRY(check_ptr(dout, "dout", g->P == 0));
+    MOE_TRY(check_ptr(a, "a", g->P == 0));
+    MOE_TRY(check_ptr(dw, "dw"));
+    MOE_TRY(check_gemm_ws(*g, ws, ws_bytes));
+    moe::GemmArgs x = gemm_args(*g);
+    x.dout = dout;
+    x.a = a;
+    x.pairs = sorted_pairs;
+    x.offsets = expert_offsets;
+    x.out = dw;
+    x.out_bf16 = dw_dtype == MOE_DTYPE_BF16;
+    x.accumulate = accumulate != 0;
+    x.ws = ws;
+    return hip_status(moe::launch_grouped_wgrad(x, stream), "grouped gemm weight gradient launch");
+}
+
+MOE_EXPORT moe_status moe_quantize_rows_int8(int64_t rows, int32_t K, const moe_bf16* x,
+                                             int8_t* codes, float* scales, hipStream_t stream) {
+    if (rows < 0 || rows > 0x7fffffffLL)
+        return fail(MOE_ERR_INVALID_ARG, "rows=%lld must be in [0, 2^31)", (long long)rows);
+    if (K <= 0 || K % 16 != 0)
+        return fail(MOE_ERR_INVALID_ARG, "K=%d must be a positive multiple of 16", K);
+    if (K > kMaxDim) return fail(MOE_ERR_UNSUPPORTED, "K=%d > %d", K, kMaxDim);
+    if (rows == 0) return ok();
+    MOE_TRY(check_ptr(x, "x"));
+    MOE_TRY(check_ptr(codes, "codes"));
+    MOE_TRY(check_ptr(scales, "scales"));
+    return hip_status(moe::launch_quantize_rows(rows, K, x, codes, scales, stream), "quantize launch");
+}
+
+MOE_EXPORT moe_status moe_grouped_gemm_int8(const moe_gemm_problem* g, const int8_t* a,
+                                            const float* a_scale, const int32_t* sorted_pairs,
+                                            const int32_t* expert_offsets, const int8_t* w,
+                                            const float* w_scale, void* out, moe_dtype out_dtype,
+                                            void* ws, size_t ws_bytes, hipStream_t stream) {
+    MOE_TRY(check_gemm(g, 16));
+    MOE_TRY(check_gemm_out(out_dtype, 0));
+    MOE_TRY(check_rows(*g, sorted_pairs));
+    if (g->P == 0) return ok();
+    MOE_TRY(check_offsets(*g, expert_offsets));
+    MOE_TRY(check_ptr(a, "a"));
+    MOE_TRY(check_ptr(a_scale, "a_scale"));
+    MOE_TRY(check_ptr(w, "w"));
+    MOE_TRY(check_ptr(w_scale, "w_scale"));
+    MOE_TRY(check_ptr(out, "out"));
+    MOE_TRY(check_gemm_ws(*g, ws, ws_bytes));
+    moe::GemmArgs x = gemm_args(*g);
+    x.a = a;
+    x.a_scale = a_scale;
+    x.w = w;
+    x.w_scale = w_scale;
+    x.pairs = sorted_pairs;
+    x.offsets = expert_offsets;
+    x.out = out;
+    x.out_bf16 = out_dtype == MOE_DTYPE_BF16;
+    x.ws = ws;
+    return hip_status(moe::launch_grouped_int8(x, stream), "grouped int8 gemm launch");
 }
 
 MOE_EXPORT const char* moe_status_string(moe_status s) {

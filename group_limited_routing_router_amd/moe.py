@@ -49,10 +49,20 @@ class MoEProblem(ctypes.Structure):
                    cfg.scale)
 
 
+class MoEGemmProblem(ctypes.Structure):
+    """moe_gemm_problem of moe_gemm.h: P sorted positions, S activation rows,
+    E experts, weights [E,N,K], k positions per activation row."""
+    _fields_ = [("P", ctypes.c_int64), ("S", ctypes.c_int64), ("E", ctypes.c_int32),
+                ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("k", ctypes.c_int32)]
+
+
 EXPORTS = ("moe_workspace_bytes", "moe_route", "moe_permute", "moe_expert_ffn",
            "moe_expert_gate_up", "moe_expert_down", "moe_combine", "moe_combine_residual",
            "moe_dense_mlp", "moe_expert_ffn_fp8", "moe_forward", "moe_forward_fp8",
            "moe_forward_noalloc", "moe_status_string", "moe_last_error",
+           # grouped products (include/moe_gemm.h)
+           "moe_gemm_workspace_bytes", "moe_grouped_gemm", "moe_grouped_gemm_dgrad",
+           "moe_grouped_gemm_wgrad", "moe_quantize_rows_int8", "moe_grouped_gemm_int8",
            # measurement kernels (include/moe_peak.h)
            "moe_peak_stream_read", "moe_peak_mfma_bf16", "moe_peak_mfma_bf16_flops",
            "moe_peak_mfma_stream", "moe_peak_mfma_stream_flops", "moe_peak_mfma_stream_bytes")
@@ -121,6 +131,20 @@ def load_library():
         lib.moe_forward.restype = st
         lib.moe_forward_noalloc.argtypes = [prob, P, P, P, P, P, P, P, ctypes.c_int, P, P, P, P]
         lib.moe_forward_noalloc.restype = st
+        gemm = ctypes.POINTER(MoEGemmProblem)
+        i32, size = ctypes.c_int, ctypes.c_size_t
+        lib.moe_gemm_workspace_bytes.argtypes = [gemm]
+        lib.moe_gemm_workspace_bytes.restype = size
+        lib.moe_grouped_gemm.argtypes = [gemm, P, P, P, P, P, i32, P, size, P]
+        lib.moe_grouped_gemm.restype = st
+        lib.moe_grouped_gemm_dgrad.argtypes = [gemm, P, P, P, P, i32, i32, P, size, P]
+        lib.moe_grouped_gemm_dgrad.restype = st
+        lib.moe_grouped_gemm_wgrad.argtypes = [gemm, P, P, P, P, P, i32, i32, P, size, P]
+        lib.moe_grouped_gemm_wgrad.restype = st
+        lib.moe_quantize_rows_int8.argtypes = [ctypes.c_int64, ctypes.c_int32, P, P, P, P]
+        lib.moe_quantize_rows_int8.restype = st
+        lib.moe_grouped_gemm_int8.argtypes = [gemm, P, P, P, P, P, P, P, i32, P, size, P]
+        lib.moe_grouped_gemm_int8.restype = st
         lib.moe_peak_stream_read.argtypes = [P, ctypes.c_size_t, ctypes.c_int, P, ctypes.c_int, P]
         lib.moe_peak_stream_read.restype = st
         lib.moe_peak_mfma_bf16.argtypes = [ctypes.c_int64, ctypes.c_int, P, ctypes.c_int, P]
@@ -259,6 +283,107 @@ def moe_forward_noalloc(p, x, w_router, bias, w_gate, w_up, w_down, out, topk_id
                                                _p(w_gate), _p(w_up), _p(w_down), _p(out),
                                                _dtype_code(out), _p(topk_ids), _p(topk_weights),
                                                _p(y), _stream(stream)))
+
+
+# ---- grouped products (include/moe_gemm.h) ----
+#
+# These also check what the C side cannot see: that each tensor has the type
+# and at least the elements the call takes, is contiguous and lies on the
+# current device.
+
+def _arg(t, name, dtype, n, nullable=False):
+    """The device address of tensor t after those checks."""
+    if t is None:
+        if nullable:
+            return None
+        raise ValueError(f"{name} is None")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} dtype {t.dtype} is not {dtype}")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current GPU")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+    if t.numel() < n:
+        raise ValueError(f"{name} has {t.numel()} elements, needs {n}")
+    return t.data_ptr()
+
+
+def _ws(ws):
+    if ws is None:
+        return None, 0
+    nbytes = ws.numel() * ws.element_size()
+    return _arg(ws, "ws", ws.dtype, 0), nbytes
+
+
+def moe_gemm_workspace_bytes(g: MoEGemmProblem) -> int:
+    return int(load_library().moe_gemm_workspace_bytes(ctypes.byref(g)))
+
+
+def moe_grouped_gemm(g, a, sorted_pairs, expert_offsets, w, out, ws=None, stream=None):
+    """out [P,N] (fp32 or bf16) = a[row(q)] . w[e]^T for each position q."""
+    code = _dtype_code(out)
+    wp, wn = _ws(ws)
+    _check(load_library().moe_grouped_gemm(
+        ctypes.byref(g), _arg(a, "a", torch.bfloat16, g.S * g.K),
+        _arg(sorted_pairs, "sorted_pairs", torch.int32, g.P, True),
+        _arg(expert_offsets, "expert_offsets", torch.int32, g.E + 1, g.E == 1),
+        _arg(w, "w", torch.bfloat16, g.E * g.N * g.K), _arg(out, "out", out.dtype, g.P * g.N),
+        code, wp, wn, _stream(stream)))
+
+
+def moe_grouped_gemm_dgrad(g, dout, expert_offsets, w, da, ws=None, accumulate=False,
+                           stream=None):
+    """da [P,K] (fp32 or bf16) = dout[q] . w[e]; da += with accumulate."""
+    code = _dtype_code(da)
+    wp, wn = _ws(ws)
+    _check(load_library().moe_grouped_gemm_dgrad(
+        ctypes.byref(g), _arg(dout, "dout", torch.bfloat16, g.P * g.N),
+        _arg(expert_offsets, "expert_offsets", torch.int32, g.E + 1, g.E == 1),
+        _arg(w, "w", torch.bfloat16, g.E * g.N * g.K), _arg(da, "da", da.dtype, g.P * g.K),
+        code, int(bool(accumulate)), wp, wn, _stream(stream)))
+
+
+def moe_grouped_gemm_wgrad(g, dout, a, sorted_pairs, expert_offsets, dw, ws=None,
+                           accumulate=False, stream=None):
+    """dw [E,N,K] (fp32 or bf16) = sum over each expert's positions of
+    dout[q]^T a[row(q)]; dw += with accumulate."""
+    code = _dtype_code(dw)
+    wp, wn = _ws(ws)
+    empty = g.P == 0
+    _check(load_library().moe_grouped_gemm_wgrad(
+        ctypes.byref(g), _arg(dout, "dout", torch.bfloat16, g.P * g.N, empty),
+        _arg(a, "a", torch.bfloat16, 0 if empty else g.S * g.K, empty),
+        _arg(sorted_pairs, "sorted_pairs", torch.int32, g.P, True),
+        _arg(expert_offsets, "expert_offsets", torch.int32, g.E + 1, g.E == 1),
+        _arg(dw, "dw", dw.dtype, g.E * g.N * g.K), code, int(bool(accumulate)), wp, wn,
+        _stream(stream)))
+
+
+def moe_quantize_rows_int8(x, codes, scales, stream=None):
+    """The rows of x [rows,K] bf16 as int8 codes [rows,K] and fp32 scales
+    [rows] (amax / 127)."""
+    if x.dim() != 2:
+        raise ValueError(f"x has {x.dim()} dimensions, needs 2")
+    rows, K = x.shape
+    _check(load_library().moe_quantize_rows_int8(
+        rows, K, _arg(x, "x", torch.bfloat16, 0), _arg(codes, "codes", torch.int8, rows * K),
+        _arg(scales, "scales", torch.float32, rows), _stream(stream)))
+
+
+def moe_grouped_gemm_int8(g, a, a_scale, sorted_pairs, expert_offsets, w, w_scale, out, ws=None,
+                          stream=None):
+    """out [P,N] (fp32 or bf16) = a_scale[row(q)] w_scale[e] (a[row(q)] .
+    w[e]^T) on int8 codes."""
+    code = _dtype_code(out)
+    wp, wn = _ws(ws)
+    _check(load_library().moe_grouped_gemm_int8(
+        ctypes.byref(g), _arg(a, "a", torch.int8, g.S * g.K),
+        _arg(a_scale, "a_scale", torch.float32, g.S),
+        _arg(sorted_pairs, "sorted_pairs", torch.int32, g.P, True),
+        _arg(expert_offsets, "expert_offsets", torch.int32, g.E + 1, g.E == 1),
+        _arg(w, "w", torch.int8, g.E * g.N * g.K),
+        _arg(w_scale, "w_scale", torch.float32, g.E * g.N), _arg(out, "out", out.dtype, g.P * g.N),
+        code, wp, wn, _stream(stream)))
 
 
 def moe_peak_stream_read(buf, sink, workgroups, nontemporal=False, stream=None):

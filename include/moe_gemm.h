@@ -1,0 +1,113 @@
+/*
+ * moe_gemm.h -- C ABI of libmoe.so: the experts' matrix products by
+ * themselves, grouped by expert with ragged sizes, with their two gradients,
+ * and in 8-bit integers with a scale for each token and each output channel.
+ *
+ * The conventions of moe.h hold: device pointers owned by the caller,
+ * contiguous, row-major, 16-byte aligned; nothing is allocated, freed or
+ * synchronised; every argument is checked on the host before anything is
+ * enqueued; no memset, so every call can be captured into a HIP graph; no
+ * atomics, so results are the same from run to run.
+ *
+ * Positions q = 0 .. P-1 are sorted by expert: expert e owns positions
+ * expert_offsets[e] .. expert_offsets[e+1]-1 (expert_offsets and sorted_pairs
+ * as moe_permute writes them).  Position q reads activation row
+ *     row(q) = sorted_pairs[q] / k,   or q where sorted_pairs is NULL.
+ * Offsets are clamped to [0, P] and rows to [0, S), so no contents of these
+ * arrays make a call read or write out of range.  Positions before
+ * expert_offsets[0] or from expert_offsets[E] on belong to no expert: their
+ * activations are not read and their output rows keep what they hold.  With
+ * E = 1, expert_offsets may be NULL: the one group then takes all P rows (a
+ * dense layer).
+ *
+ * A row that holds an infinity or NaN affects its own output row alone (in
+ * the weight gradient, its own expert's gradient).
+ */
+#ifndef MOE_GEMM_H
+#define MOE_GEMM_H
+
+#include "moe.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Shape of a grouped product.
+ *   P  sorted positions (>= 0, fits in int32)
+ *   S  rows of the activations a (S >= P where sorted_pairs is NULL)
+ *   E  experts, 1 <= E <= 256
+ *   N, K  the weights are [E,N,K]; multiples of 8 (of 16 for the int8
+ *      product), at most 65536
+ *   k  positions per activation row, >= 1: row(q) = sorted_pairs[q] / k */
+typedef struct moe_gemm_problem {
+    int64_t P, S;
+    int32_t E, N, K, k;
+} moe_gemm_problem;
+
+/* Bytes of scratch the calls below need in `ws` for problem g (0 if g is
+ * invalid, or if none is needed: ws may then be NULL).  One workspace sized
+ * by this function serves every call on g; what it holds before a call does
+ * not matter.  Calls that overlap need one workspace each. */
+size_t moe_gemm_workspace_bytes(const moe_gemm_problem* g);
+
+/* The product: out[q,n] = sum_k a[row(q),k] * w[e,n,k], e the expert that
+ * owns q.
+ *   a    [S,K] bf16
+ *   w    [E,N,K] bf16
+ *   out  [P,N] fp32 or bf16 (out_dtype): summed in fp32, rounded once */
+moe_status moe_grouped_gemm(const moe_gemm_problem* g, const moe_bf16* a,
+                            const int32_t* sorted_pairs, const int32_t* expert_offsets,
+                            const moe_bf16* w, void* out, moe_dtype out_dtype, void* ws,
+                            size_t ws_bytes, hipStream_t stream);
+
+/* The gradient of the product's input, position by position:
+ *     da[q,k] = sum_n dout[q,n] * w[e,n,k]
+ *   dout [P,N] bf16 in sorted order
+ *   da   [P,K] fp32 or bf16 in sorted order (the sum over the k positions of
+ *        one activation row is moe_combine with weights of one)
+ *   accumulate  not 0: da += (fp32 only) */
+moe_status moe_grouped_gemm_dgrad(const moe_gemm_problem* g, const moe_bf16* dout,
+                                  const int32_t* expert_offsets, const moe_bf16* w, void* da,
+                                  moe_dtype da_dtype, int accumulate, void* ws, size_t ws_bytes,
+                                  hipStream_t stream);
+
+/* The gradient of the product's weights:
+ *     dw[e,n,k] = sum over e's positions q of dout[q,n] * a[row(q),k]
+ *   dout [P,N] bf16 in sorted order;  a [S,K] bf16
+ *   dw   [E,N,K] fp32 or bf16; zero for an expert without positions
+ *   accumulate  not 0: dw += (fp32 only)
+ * With P = 0, dout, a and sorted_pairs may be NULL; dw is still written. */
+moe_status moe_grouped_gemm_wgrad(const moe_gemm_problem* g, const moe_bf16* dout,
+                                  const moe_bf16* a, const int32_t* sorted_pairs,
+                                  const int32_t* expert_offsets, void* dw, moe_dtype dw_dtype,
+                                  int accumulate, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Rows of bf16 as 8-bit integers with one fp32 scale each:
+ *     amax = max_k |x[r,k]|,  scales[r] = amax / 127,
+ *     codes[r,k] = 127 x[r,k] / amax, rounded to the nearest integer (ties to
+ *     even; the quotient is the correctly rounded fp32 one)
+ * A row of zeros gets the scale 1 and codes 0; so does a row whose amax is
+ * below 2^-100.  A row that holds an infinity or NaN gets the scale NaN and
+ * codes 0.
+ *   x [rows,K] bf16;  codes [rows,K] int8;  scales [rows] fp32
+ *   rows >= 0, K a multiple of 16, K <= 65536 */
+moe_status moe_quantize_rows_int8(int64_t rows, int32_t K, const moe_bf16* x, int8_t* codes,
+                                  float* scales, hipStream_t stream);
+
+/* The product in 8-bit integers:
+ *     out[q,n] = (a_scale[row(q)] * w_scale[e,n])
+ *                * sum_k a[row(q),k] * w[e,n,k]
+ * The sum is exact (int32); the scales multiply it in fp32.
+ *   a [S,K] int8 codes, a_scale [S] fp32;  w [E,N,K] int8 codes, w_scale
+ *   [E,N] fp32;  out [P,N] fp32 or bf16.  N and K multiples of 16. */
+moe_status moe_grouped_gemm_int8(const moe_gemm_problem* g, const int8_t* a, const float* a_scale,
+                                 const int32_t* sorted_pairs, const int32_t* expert_offsets,
+                                 const int8_t* w, const float* w_scale, void* out,
+                                 moe_dtype out_dtype, void* ws, size_t ws_bytes,
+                                 hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MOE_GEMM_H */
