@@ -7,13 +7,11 @@
 //   weight grad  dw[e,n,k] = sum_{q of e} dout[q,n] a[row(q),k]
 //   int8         out[q,n]  = a_scale[row(q)] w_scale[e,n] sum_k a[row(q),k] w[e,n,k]
 #include "common.h"
+#include "gemm_tile.h"
 #include "kernels.h"
-#include "tiles.h"
 
 namespace moe {
 namespace {
-
-enum Mode { kProduct = 0, kInputGrad = 1, kWeightGrad = 2 };
 
 // The rows of the sorted order that expert e owns, clamped to [0, P].
 __device__ __forceinline__ void expert_rows(const GemmArgs& g, int e, int64_t& first, int64_t& n) {
@@ -159,6 +157,49 @@ hipError_t launch_plain(const GemmArgs& g, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Workgroups of a tiled launch (an upper bound: the host does not read the
+// experts' counts).
+template <int MODE, int BX, int BY>
+int64_t tile_grid(const GemmArgs& g) {
+    const int64_t cols = MODE == kProduct ? g.N : g.K;
+    const int64_t row_tiles = MODE == kWeightGrad ? static_cast<int64_t>((g.N + BY - 1) / BY) * g.E
+                                                  : (g.P + BY - 1) / BY + (g.E < g.P ? g.E : g.P);
+    const int64_t tiles = row_tiles * ((cols + BX - 1) / BX);
+    return (tiles + kNumXcd - 1) / kNumXcd * kNumXcd;
+}
+
+template <int MODE, bool I8, int BX, int BY>
+hipError_t launch_tiles(const GemmArgs& g, hipStream_t s) {
+    const int64_t grid = tile_grid<MODE, BX, BY>(g);
+    if (grid <= 0) return hipSuccess;
+    if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+    const dim3 blocks(static_cast<unsigned>(grid)), threads(kThreads);
+    if constexpr (MODE != kInputGrad) {
+        if (g.pairs) {
+            gemm_tile_kernel<MODE, I8, BX, BY, true><<<blocks, threads, 0, s>>>(g);
+            return hipGetLastError();
+        }
+    }
+    gemm_tile_kernel<MODE, I8, BX, BY, false><<<blocks, threads, 0, s>>>(g);
+    return hipGetLastError();
+}
+
+template <int MODE, bool I8>
+hipError_t launch(const GemmArgs& g, hipStream_t s) {
+    // gathered rows are addressed with 32-bit offsets from a
+    if (g.pairs && g.S * static_cast<int64_t>(g.K) * (I8 ? 1 : 2) > static_cast<int64_t>(kNoRowOffset))
+        return launch_plain<MODE, I8>(g, s);
+    // 256 x 256 tiles move half the operand bytes of 128 x 128 ones (8192
+    // tokens over 256 experts: product 1.95 against 2.36 ms), but need about
+    // two tiles for each compute unit (5003 rows, 24 experts, 1000 x 776: 30
+    // against 21 us), and with few rows the smaller tile streams the weights
+    // faster (128 tokens over 256 experts: 1.08 against 1.10 ms).
+    const int64_t mean_rows = g.P / g.E;
+    if (tile_grid<MODE, 256, 256>(g) >= 512 && (MODE == kWeightGrad || mean_rows > 32))
+        return launch_tiles<MODE, I8, 256, 256>(g, s);
+    return launch_tiles<MODE, I8, 128, 128>(g, s);
+}
+
 // One row of bf16 per workgroup: its largest magnitude, then its codes.
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const uint16_t* x, int K, int8_t* codes,
                                                                  float* scales) {
@@ -210,13 +251,13 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const uint16_t*
 
 size_t grouped_ws_bytes(const GemmArgs&) { return 0; }
 
-hipError_t launch_grouped_gemm(const GemmArgs& g, hipStream_t s) { return launch_plain<kProduct, false>(g, s); }
+hipError_t launch_grouped_gemm(const GemmArgs& g, hipStream_t s) { return launch<kProduct, false>(g, s); }
 
-hipError_t launch_grouped_dgrad(const GemmArgs& g, hipStream_t s) { return launch_plain<kInputGrad, false>(g, s); }
+hipError_t launch_grouped_dgrad(const GemmArgs& g, hipStream_t s) { return launch<kInputGrad, false>(g, s); }
 
-hipError_t launch_grouped_wgrad(const GemmArgs& g, hipStream_t s) { return launch_plain<kWeightGrad, false>(g, s); }
+hipError_t launch_grouped_wgrad(const GemmArgs& g, hipStream_t s) { return launch<kWeightGrad, false>(g, s); }
 
-hipError_t launch_grouped_int8(const GemmArgs& g, hipStream_t s) { return launch_plain<kProduct, true>(g, s); }
+hipError_t launch_grouped_int8(const GemmArgs& g, hipStream_t s) { return launch<kProduct, true>(g, s); }
 
 hipError_t launch_quantize_rows(int64_t rows, int K, const uint16_t* x, int8_t* codes, float* scales,
                                 hipStream_t s) {

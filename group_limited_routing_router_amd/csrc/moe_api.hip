@@ -474,7 +474,8 @@ MOE_EXPORT moe_status moe_forward_noalloc(const moe_problem* p, const moe_bf16* 
 
 namespace {
 
-moe_status check_gemm(const moe_gemm_problem* g, int multiple) {
+// k_multiple: elements of the operands in 16 bytes.
+moe_status check_gemm(const moe_gemm_problem* g, int k_multiple) {
     if (!g) return fail(MOE_ERR_INVALID_ARG, "problem is NULL");
     if (g->P < 0 || g->P > 0x7fffffffLL)
         return fail(MOE_ERR_INVALID_ARG, "P=%lld must be in [0, 2^31)", (long long)g->P);
@@ -482,10 +483,10 @@ moe_status check_gemm(const moe_gemm_problem* g, int multiple) {
         return fail(MOE_ERR_INVALID_ARG, "S=%lld must be in [0, 2^31)", (long long)g->S);
     if (g->E <= 0) return fail(MOE_ERR_INVALID_ARG, "E=%d must be positive", g->E);
     if (g->k < 1) return fail(MOE_ERR_INVALID_ARG, "k=%d must be positive", g->k);
-    if (g->N <= 0 || g->N % multiple != 0)
-        return fail(MOE_ERR_INVALID_ARG, "N=%d must be a positive multiple of %d", g->N, multiple);
-    if (g->K <= 0 || g->K % multiple != 0)
-        return fail(MOE_ERR_INVALID_ARG, "K=%d must be a positive multiple of %d", g->K, multiple);
+    if (g->N <= 0 || g->N % 8 != 0)
+        return fail(MOE_ERR_INVALID_ARG, "N=%d must be a positive multiple of 8", g->N);
+    if (g->K <= 0 || g->K % k_multiple != 0)
+        return fail(MOE_ERR_INVALID_ARG, "K=%d must be a positive multiple of %d", g->K, k_multiple);
     if (g->E > 256) return fail(MOE_ERR_UNSUPPORTED, "E=%d > 256", g->E);
     if (g->N > kMaxDim) return fail(MOE_ERR_UNSUPPORTED, "N=%d > %d", g->N, kMaxDim);
     if (g->K > kMaxDim) return fail(MOE_ERR_UNSUPPORTED, "K=%d > %d", g->K, kMaxDim);

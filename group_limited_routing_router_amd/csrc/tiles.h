@@ -49,15 +49,18 @@ constexpr uint32_t kNoRowOffset = 0xFFF00000u;
 // GRAN = 1 splits an expert's rows evenly over its row tiles; GRAN > 1 gives
 // every row tile but the last the same multiple of GRAN rows (for the large
 // tile, whose two row waves take alternate 32-row blocks: 64-row multiples
-// keep them equally busy).  Returns false for surplus workgroups (uniform
+// keep them equally busy).  BAND > 0 orders an expert's tiles in bands of that
+// many row tiles (column by column inside a band) instead of all row tiles of
+// a column.  offsets may be NULL: one expert with all P rows.  Returns false
+// for surplus workgroups (uniform
 // over the workgroup).  s_off holds kMaxE + 1 entries, s_tstart
 // kMaxE + 1 + kWaves.
-template <int BM, int GRAN = 1>
+template <int BM, int GRAN = 1, int BAND = 0>
 __device__ bool find_tile(const int32_t* offsets, int64_t P, int E, int ncol_tiles, int32_t* s_off,
                           int32_t* s_tstart, int& e_out, int& nt_out, int& row0_out, int& rows_out) {
     const int tid = threadIdx.x;
     for (int e = tid; e <= E; e += kThreads) {
-        int64_t o = offsets[e];
+        int64_t o = offsets ? offsets[e] : (e == 0 ? 0 : P);
         o = o < 0 ? 0 : (o > P ? P : o);
         s_off[e] = static_cast<int32_t>(o);
     }
@@ -102,8 +105,18 @@ __device__ bool find_tile(const int32_t* offsets, int64_t P, int E, int ncol_til
     const int e = expert_at(pos);
     const int tiles_e = s_tstart[pos + 1] - s_tstart[pos];  // >= 1 for the position found
     const int64_t rel = L - static_cast<int64_t>(s_tstart[pos]) * ncol_tiles;
-    const int nt = static_cast<int>(rel / tiles_e);
-    const int mt = static_cast<int>(rel - static_cast<int64_t>(nt) * tiles_e);
+    int nt, mt;
+    if constexpr (BAND > 0) {
+        const int64_t per_band = static_cast<int64_t>(BAND) * ncol_tiles;
+        const int band = static_cast<int>(rel / per_band);
+        const int in = static_cast<int>(rel - band * per_band);
+        const int high = min(BAND, tiles_e - band * BAND);
+        nt = in / high;
+        mt = band * BAND + in % high;
+    } else {
+        nt = static_cast<int>(rel / tiles_e);
+        mt = static_cast<int>(rel - static_cast<int64_t>(nt) * tiles_e);
+    }
     const int n_e = s_off[e + 1] - s_off[e];
     e_out = e;
     nt_out = nt;

@@ -36,7 +36,7 @@ extern "C" {
  *   P  sorted positions (>= 0, fits in int32)
  *   S  rows of the activations a (S >= P where sorted_pairs is NULL)
  *   E  experts, 1 <= E <= 256
- *   N, K  the weights are [E,N,K]; multiples of 8 (of 16 for the int8
+ *   N, K  the weights are [E,N,K]; multiples of 8 (K of 16 for the int8
  *      product), at most 65536
  *   k  positions per activation row, >= 1: row(q) = sorted_pairs[q] / k */
 typedef struct moe_gemm_problem {
@@ -99,7 +99,7 @@ moe_status moe_quantize_rows_int8(int64_t rows, int32_t K, const moe_bf16* x, in
  *                * sum_k a[row(q),k] * w[e,n,k]
  * The sum is exact (int32); the scales multiply it in fp32.
  *   a [S,K] int8 codes, a_scale [S] fp32;  w [E,N,K] int8 codes, w_scale
- *   [E,N] fp32;  out [P,N] fp32 or bf16.  N and K multiples of 16. */
+ *   [E,N] fp32;  out [P,N] fp32 or bf16.  K a multiple of 16. */
 moe_status moe_grouped_gemm_int8(const moe_gemm_problem* g, const int8_t* a, const float* a_scale,
                                  const int32_t* sorted_pairs, const int32_t* expert_offsets,
                                  const int8_t* w, const float* w_scale, void* out,
