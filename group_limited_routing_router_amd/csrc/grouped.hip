@@ -8,6 +8,7 @@
 //   int8         out[q,n]  = a_scale[row(q)] w_scale[e,n] sum_k a[row(q),k] w[e,n,k]
 #include "common.h"
 #include "gemm_tile.h"
+#include "gemm_wgrad.h"
 #include "kernels.h"
 
 namespace moe {
@@ -184,6 +185,21 @@ hipError_t launch_tiles(const GemmArgs& g, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <int BX, int BY, bool GATHER>
+hipError_t launch_wgrad(const GemmArgs& g, hipStream_t s) {
+    const int64_t tiles = static_cast<int64_t>((g.K + BX - 1) / BX) * ((g.N + BY - 1) / BY) * g.E;
+    const int64_t most = static_cast<int64_t>(kNumCu) * WgradShape<BX, BY, GATHER>::kPerCu;
+    const int64_t grid = tiles < most ? (tiles + kNumXcd - 1) / kNumXcd * kNumXcd : most;
+    const dim3 blocks(static_cast<unsigned>(grid)), threads(kThreads);
+    if (g.out_bf16)
+        gemm_wgrad_kernel<BX, BY, GATHER, true, false><<<blocks, threads, 0, s>>>(g);
+    else if (g.accumulate)
+        gemm_wgrad_kernel<BX, BY, GATHER, false, true><<<blocks, threads, 0, s>>>(g);
+    else
+        gemm_wgrad_kernel<BX, BY, GATHER, false, false><<<blocks, threads, 0, s>>>(g);
+    return hipGetLastError();
+}
+
 template <int MODE, bool I8>
 hipError_t launch(const GemmArgs& g, hipStream_t s) {
     // gathered rows are addressed with 32-bit offsets from a
@@ -195,6 +211,11 @@ hipError_t launch(const GemmArgs& g, hipStream_t s) {
     // against 21 us), and with few rows the smaller tile streams the weights
     // faster (128 tokens over 256 experts: 1.08 against 1.10 ms).
     const int64_t mean_rows = g.P / g.E;
+    if constexpr (MODE == kWeightGrad) {
+        const bool big = tile_grid<MODE, 256, 256>(g) >= 512;
+        if (g.pairs) return big ? launch_wgrad<256, 256, true>(g, s) : launch_wgrad<128, 128, true>(g, s);
+        return big ? launch_wgrad<256, 256, false>(g, s) : launch_wgrad<128, 128, false>(g, s);
+    }
     if (tile_grid<MODE, 256, 256>(g) >= 512 && (MODE == kWeightGrad || mean_rows > 32))
         return launch_tiles<MODE, I8, 256, 256>(g, s);
     return launch_tiles<MODE, I8, 128, 128>(g, s);

@@ -18,6 +18,8 @@ struct GemmArgs {
     int64_t S;               // rows of a
     int E, N, K;             // w is [E,N,K]
     int k;                   // row(q) = pairs[q] / k
+    uint32_t k_magic;        // p / k = umulhi(p, k_magic) >> k_shift for 0 <= p < 2^31
+    int k_shift;             // (k = 1: k_shift < 0)
     const void* a;           // activations [S,K]: bf16 or int8 codes
     const void* dout;        // output gradient [P,N] bf16 (the two gradients)
     const void* w;           // weights [E,N,K]: bf16 or int8 codes

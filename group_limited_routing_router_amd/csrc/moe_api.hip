@@ -523,6 +523,12 @@ moe::GemmArgs gemm_args(const moe_gemm_problem& g) {
     a.N = g.N;
     a.K = g.K;
     a.k = g.k;
+    // 2^(31 + b) / k rounded up, b = ceil(log2 k): a 32-bit multiplier that
+    // gives the exact quotient of every 31-bit dividend
+    int b = 0;
+    while ((1LL << b) < g.k) ++b;
+    a.k_magic = static_cast<uint32_t>((1ULL << (31 + b)) / static_cast<uint64_t>(g.k) + 1);
+    a.k_shift = b - 1;
     return a;
 }
 
