@@ -1,7 +1,8 @@
 // gemm_tile.h -- the tiled kernel of the grouped products (moe_gemm.h).
 //
-// A workgroup of 4 waves owns a BY x BX tile of one expert's output: BY rows
-// (positions of the expert, or rows n of its weight gradient) by BX columns.
+// The product and the input gradient (the weight gradient: gemm_wgrad.h).
+// A workgroup of 4 waves owns a BY x BX tile of one expert's output: BY
+// positions of the expert by BX columns.
 // Each wave owns a quarter, 32 x 32 blocks dealt over the two wave rows
 // (block b to wave row b % 2), blocks past the tile's last row skipped, so a
 // partly filled tile costs matrix time in proportion to its rows.
@@ -10,7 +11,6 @@
 //              X (columns)                 Y (rows)
 //   product    w[e], reduction along rows  a, reduction along rows (gathered)
 //   input grad w[e], reduction down rows   dout, reduction along rows
-//   weight grad a, down rows (gathered)    dout, down rows
 // X is the first operand of the matrix instruction, so a lane ends with one
 // output row and groups of four consecutive columns of it.
 //
@@ -20,13 +20,15 @@
 //  - reduction along the rows in memory: the stage holds 128 bytes of each
 //    row, chunk c (16 bytes) of row r at place c ^ ((r >> 1) & 7), so the 16
 //    rows of an operand read lie on all 64 banks once;
-//  - reduction down the rows: the stage holds 64 rows of BX (BY) elements,
+//  - reduction down the rows: the stage holds 64 rows of BX elements,
 //    chunk c of row r at place c ^ tr_swizzle(r), and the operand is read
 //    with the transposing LDS load (ds_read_b64_tr_b16: in each group of 16
 //    lanes, lane i reads 4 elements of row i / 4 and receives column i of
 //    the 4 x 16 block).  The swizzle puts the 4 rows x 64 bytes that 32 lanes
 //    read on all 64 banks once.
-// X is loaded two stages ahead into three buffers, Y one ahead into two.
+// X is loaded two stages ahead into three buffers, Y one ahead into two; the
+// 32-row tile (few rows, where the weight stream is all the time there is)
+// loads both three stages ahead into four.
 // The compiler does not see these loads: the kernel waits for them (vmcnt)
 // before each stage's barrier, and for all of them before it goes on to its
 // epilogue.
@@ -63,37 +65,37 @@ __device__ __forceinline__ u32x2 lds_read_tr(const unsigned char* p) {
 // high, which share both operands in its L2.
 constexpr int kBand = 8;
 
-// Rows of the gathered operand whose offsets are kept in LDS at a time
-// (weight gradient).
-constexpr int kGatherRows = 4096;
-
-template <int MODE, bool I8, int BX, int BY, bool GATHER>
+template <int BX, int BY>
 struct TileShape {
-    static constexpr bool kTrX = MODE != kProduct, kTrY = MODE == kWeightGrad;
-    static constexpr bool kIndex = MODE == kWeightGrad && GATHER;
-    static constexpr int kXBufs = kIndex ? 2 : 3, kYBufs = 2;
+    static constexpr int kWavesY = BY >= 64 ? 2 : 1, kWavesX = kWaves / kWavesY;
+    static constexpr int kXBufs = BY >= 64 ? 3 : 4, kYBufs = BY >= 64 ? 2 : 4;
     static constexpr int kXStage = BX * 128, kYStage = BY * 128;
-    static constexpr int kArena = kXBufs * kXStage + kYBufs * kYStage + (kIndex ? kGatherRows * 4 : 0);
+    static constexpr int kArena = kXBufs * kXStage + kYBufs * kYStage;
     static_assert(kArena <= 163840, "LDS budget");
     static constexpr int kPerCu = kArena <= 81920 ? 2 : 1;
 };
 
-template <int MODE, bool I8, int BX, int BY, bool GATHER>
-__global__ __launch_bounds__(kThreads, (TileShape<MODE, I8, BX, BY, GATHER>::kPerCu)) void gemm_tile_kernel(GemmArgs g) {
-    typedef TileShape<MODE, I8, BX, BY, GATHER> Shape;
-    constexpr bool TRX = Shape::kTrX, TRY = Shape::kTrY, INDEX = Shape::kIndex;
+template <int MODE, bool I8, int BX, int BY, bool GATHER, bool NT>
+__global__ __launch_bounds__(kThreads, (TileShape<BX, BY>::kPerCu)) void gemm_tile_kernel(GemmArgs g) {
+    typedef TileShape<BX, BY> Shape;
+    constexpr bool TRX = MODE == kInputGrad;
     constexpr int EB = I8 ? 1 : 2;             // bytes per operand element
     constexpr int SK = 128 / EB;               // reduction per stage
-    constexpr int XB = BX / 64, YB = BY / 64;  // 32-blocks per wave
+    constexpr int WY = Shape::kWavesY, WX = Shape::kWavesX;
+    constexpr int XB = BX / 32 / WX, YB = BY / 32 / WY;  // 32-blocks per wave
     constexpr int XS = Shape::kXStage, YS = Shape::kYStage;
-    constexpr int XBUFS = Shape::kXBufs;
-    constexpr int DMA_X = BX / 32, DMA_Y = BY / 32;  // 1 KB loads per wave and stage
+    constexpr int XBUFS = Shape::kXBufs, YBUFS = Shape::kYBufs;
+    constexpr int XA = XBUFS - 1, YA = YBUFS - 1;        // stages the loads run ahead
+    constexpr int DMA_X = BX / 32, DMA_Y = BY / 32;      // 1 KB loads per wave and stage
+    // loads younger than those of the next stage, at a stage's end: each stage
+    // loads Y first, then X
+    constexpr int YOUNGER = YA == 1 ? DMA_X : (XA - 1) * (DMA_X + DMA_Y);
+    static_assert(YA == 1 ? XA >= 1 : XA == YA, "the count above");
     static_assert(!TRX || !I8, "the transposing load is for 16-bit elements");
     typedef typename std::conditional<I8, i32x16, f32x16>::type Acc;
 
     __shared__ __attribute__((aligned(1024))) unsigned char s_arena[Shape::kArena];
     const uint32_t arena = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(s_arena));
-    uint32_t* s_index = reinterpret_cast<uint32_t*>(s_arena + XBUFS * XS + Shape::kYBufs * YS);
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -101,57 +103,29 @@ __global__ __launch_bounds__(kThreads, (TileShape<MODE, I8, BX, BY, GATHER>::kPe
     const int cols = MODE == kProduct ? g.N : g.K;
     const int col_tiles = (cols + BX - 1) / BX;
 
-    // ---- this workgroup's tile: output rows [orow0, orow0 + rows) of the
-    // expert's output, columns from c0; reduction [0, red) ----
-    int e, c0, rows, red;
-    int64_t orow0;  // first output row: sorted position, or e * N + n
-    int64_t first;  // weight grad: first position of the expert
-    if constexpr (MODE == kWeightGrad) {
-        const int row_tiles = (g.N + BY - 1) / BY;
-        const int per_expert = row_tiles * col_tiles;
-        // each XCD takes a contiguous run of the tiles, expert by expert
-        const int64_t total = static_cast<int64_t>(per_expert) * g.E;
-        const int xcd = blockIdx.x % kNumXcd;
-        const int64_t local = blockIdx.x / kNumXcd, per = total / kNumXcd, rem = total % kNumXcd;
-        if (local >= per + (xcd < rem ? 1 : 0)) return;
-        const int64_t L = xcd * per + (xcd < rem ? xcd : rem) + local;
-        const int pos = static_cast<int>(L / per_expert), in = static_cast<int>(L % per_expert);
-        e = g.E % kNumXcd == 0 ? (pos % kNumXcd) * (g.E / kNumXcd) + pos / kNumXcd : pos;
-        const int band = in / (kBand * col_tiles), in_band = in % (kBand * col_tiles);
-        const int high = min(kBand, row_tiles - band * kBand);
-        c0 = in_band / high * BX;
-        const int n0 = (band * kBand + in_band % high) * BY;
-        rows = min(BY, g.N - n0);
-        orow0 = static_cast<int64_t>(e) * g.N + n0;
-        int64_t b = 0, t = g.P;
-        if (g.offsets) {
-            b = g.offsets[e];
-            t = g.offsets[e + 1];
-            b = b < 0 ? 0 : (b > g.P ? g.P : b);
-            t = t < 0 ? 0 : (t > g.P ? g.P : t);
-        }
-        first = b;
-        red = static_cast<int>(t > b ? t - b : 0);
-        if (red == 0 && g.accumulate) return;
-    } else {
+    // ---- this workgroup's tile: output rows [row0, row0 + rows), columns
+    // from c0; reduction [0, red) ----
+    int e, nt, row0, rows;
+    {
         int32_t* s_off = reinterpret_cast<int32_t*>(s_arena);
         int32_t* s_tstart = s_off + (kMaxE + 1);
-        int nt, row0;
-        if (!find_tile<BY, 64, kBand>(g.offsets, g.P, g.E, col_tiles, s_off, s_tstart, e, nt, row0, rows)) return;
+        if (!find_tile<BY, BY >= 64 ? 64 : 1, kBand>(g.offsets, g.P, g.E, col_tiles, s_off, s_tstart, e, nt, row0, rows)) return;
         // the same in every lane: kept in scalar registers
         e = __builtin_amdgcn_readfirstlane(e);
         nt = __builtin_amdgcn_readfirstlane(nt);
         row0 = __builtin_amdgcn_readfirstlane(row0);
         rows = __builtin_amdgcn_readfirstlane(rows);
         __syncthreads();  // everyone is done with the schedule before the arena is reused
-        c0 = nt * BX;
-        orow0 = row0;
-        first = row0;
-        red = MODE == kProduct ? g.K : g.N;
     }
+    const int c0 = nt * BX;
+    const int red = MODE == kProduct ? g.K : g.N;
+    const int64_t orow0 = row0;
     const int nblk = (rows + 31) >> 5;
     const int nk = (red + SK - 1) / SK;
-    const int n0 = MODE == kWeightGrad ? static_cast<int>(orow0 - static_cast<int64_t>(e) * g.N) : 0;
+    // a split reduction: this workgroup's stages [s0, s1); its sums go to ws
+    const int s0 = static_cast<int>(static_cast<int64_t>(nk) * blockIdx.y / gridDim.y);
+    const int s1 = static_cast<int>(static_cast<int64_t>(nk) * (blockIdx.y + 1) / gridDim.y);
+    const bool split = gridDim.y > 1;
 
     // ---- loads.  Along rows: wave w fills rows [w R, w R + R) of a stage (R =
     // BX / 4), 8 rows a load; lane L of load j writes row w R + 8 j + L / 8,
@@ -162,18 +136,13 @@ __global__ __launch_bounds__(kThreads, (TileShape<MODE, I8, BX, BY, GATHER>::kPe
     uint32_t vx[DMA_X], vy[DMA_Y];
     const int64_t K = g.K, N = g.N;
     const unsigned char* wmat = static_cast<const unsigned char*>(g.w) + static_cast<int64_t>(e) * N * K * EB;
-    if constexpr (MODE == kProduct)
+    if constexpr (MODE == kProduct) {
         xbase = wmat + static_cast<int64_t>(c0) * K * EB;
-    else if constexpr (MODE == kInputGrad)
-        xbase = wmat + static_cast<int64_t>(c0) * 2;
-    else
-        xbase = static_cast<const unsigned char*>(g.a) + (INDEX ? 0 : first * K * 2) + static_cast<int64_t>(c0) * 2;
-    if constexpr (MODE == kProduct)
         ybase = static_cast<const unsigned char*>(g.a) + (GATHER ? 0 : orow0 * K * EB);
-    else if constexpr (MODE == kInputGrad)
+    } else {
+        xbase = wmat + static_cast<int64_t>(c0) * 2;
         ybase = static_cast<const unsigned char*>(g.dout) + orow0 * N * 2;
-    else
-        ybase = static_cast<const unsigned char*>(g.dout) + (first * N + n0) * 2;
+    }
     auto along_row = [&](int j, int per_wave) { return wave * per_wave + j * 8 + (lane >> 3); };
     auto along_chunk = [&](int r) { return (lane & 7) ^ ((r >> 1) & 7); };
     auto down_row = [&](int j, int chunks) { return wave * 16 + j * (64 / chunks) + lane / chunks; };
@@ -182,7 +151,7 @@ __global__ __launch_bounds__(kThreads, (TileShape<MODE, I8, BX, BY, GATHER>::kPe
         if constexpr (TRX) {
             const int r = down_row(j, BX / 8);
             const int c = (lane % (BX / 8)) ^ tr_swizzle(r);
-            vx[j] = INDEX ? static_cast<uint32_t>(c * 16) : static_cast<uint32_t>(r * K * 2 + c * 16);
+            vx[j] = static_cast<uint32_t>(r * K * 2 + c * 16);
         } else {
             const int r = along_row(j, BX / 4);
             vx[j] = static_cast<uint32_t>(r * K * EB + along_chunk(r) * 16);
@@ -190,74 +159,53 @@ __global__ __launch_bounds__(kThreads, (TileShape<MODE, I8, BX, BY, GATHER>::kPe
     }
 #pragma unroll
     for (int j = 0; j < DMA_Y; ++j) {
-        if constexpr (TRY) {
-            const int r = down_row(j, BY / 8);
-            vy[j] = static_cast<uint32_t>(r * N * 2 + ((lane % (BY / 8)) ^ tr_swizzle(r)) * 16);
+        const int r = along_row(j, BY / 4);
+        const int c = along_chunk(r);
+        const int64_t ld = MODE == kProduct ? K * EB : N * 2;
+        if (r >= nblk * 32) {
+            vy[j] = kNoRowOffset;
+        } else if (GATHER) {
+            int64_t s = g.pairs[orow0 + min(r, rows - 1)] / g.k;
+            s = s < 0 ? 0 : (s >= g.S ? g.S - 1 : s);
+            vy[j] = static_cast<uint32_t>(s * ld + c * 16);
         } else {
-            const int r = along_row(j, BY / 4);
-            const int c = along_chunk(r);
-            const int64_t ld = MODE == kProduct ? K * EB : N * 2;
-            if (r >= nblk * 32) {
-                vy[j] = kNoRowOffset;
-            } else if (GATHER) {
-                int64_t s = g.pairs[orow0 + min(r, rows - 1)] / g.k;
-                s = s < 0 ? 0 : (s >= g.S ? g.S - 1 : s);
-                vy[j] = static_cast<uint32_t>(s * ld + c * 16);
-            } else {
-                vy[j] = static_cast<uint32_t>(r * ld + c * 16);
-            }
+            vy[j] = static_cast<uint32_t>(r * ld + c * 16);
         }
     }
     // chunks of the last stage that lie inside the reduction (along rows)
     const int tail = (red - (nk - 1) * SK) / (16 / EB);
     auto x_buf = [&](int i) { return arena + i * XS; };
     auto y_buf = [&](int i) { return arena + XBUFS * XS + i * YS; };
-    // down rows: the buffer starts at the stage's first row and ends with its
-    // last row inside the reduction
-    auto down_rsrc = [&](const unsigned char* base, int64_t ld, int col, int kt) {
-        const int valid = min(SK, red - kt * SK);
-        return make_rsrc(base + static_cast<int64_t>(kt) * SK * ld * 2,
-                         static_cast<uint32_t>((valid * ld - col) * 2));
-    };
     const __amdgpu_buffer_rsrc_t rsrc_x0 =
-        MODE == kProduct ? make_rsrc(xbase, static_cast<uint32_t>(min(BX, cols - c0) * K * EB))
-                         : make_rsrc(xbase, static_cast<uint32_t>(INDEX ? (g.S * K - c0) * 2 : 0));
+        make_rsrc(xbase, static_cast<uint32_t>(TRX ? 0 : min(BX, cols - c0) * K * EB));
     const __amdgpu_buffer_rsrc_t rsrc_y0 = make_rsrc(
         ybase, static_cast<uint32_t>(MODE == kProduct ? (GATHER ? g.S : rows) * K * EB : rows * N * 2));
-    int stage0 = 0;           // first stage of the chunk of rows whose offsets are in LDS
-    uint32_t ix[DMA_X];       // INDEX: the next stage's row offsets
-    auto load_index = [&](int kt) {
-        if constexpr (INDEX) {
-#pragma unroll
-            for (int j = 0; j < DMA_X; ++j) ix[j] = s_index[(kt - stage0) * SK + down_row(j, BX / 8)];
-        }
-    };
     auto dma_x = [&](int j, int buf, int kt) {
         const uint32_t at = x_buf(buf) + wave * (XS / 4) + j * 1024;
-        if constexpr (INDEX) {
-            dma_load16(at, rsrc_x0, ix[j] + vx[j], 0);
-        } else if constexpr (TRX) {
-            dma_load16(at, down_rsrc(xbase, K, c0, kt), vx[j], 0);
+        if constexpr (TRX) {
+            // the buffer starts at the stage's first row and ends with its
+            // last row inside the reduction
+            const int valid = min(SK, red - kt * SK);
+            dma_load16<NT>(at,
+                       make_rsrc(xbase + static_cast<int64_t>(kt) * SK * K * 2,
+                                 static_cast<uint32_t>((valid * K - c0) * 2)),
+                       vx[j], 0);
         } else {
             const bool past = kt == nk - 1 && along_chunk(along_row(j, BX / 4)) >= tail;
-            dma_load16(at, rsrc_x0, past ? kNoRowOffset : vx[j], static_cast<uint32_t>(kt * 128));
+            dma_load16<NT>(at, rsrc_x0, past ? kNoRowOffset : vx[j], static_cast<uint32_t>(kt * 128));
         }
     };
     auto dma_y = [&](int j, int buf, int kt) {
         const uint32_t at = y_buf(buf) + wave * (YS / 4) + j * 1024;
-        if constexpr (TRY) {
-            dma_load16(at, down_rsrc(ybase, N, n0, kt), vy[j], 0);
-        } else {
-            const bool past = kt == nk - 1 && along_chunk(along_row(j, BY / 4)) >= tail;
-            dma_load16(at, rsrc_y0, past ? kNoRowOffset : vy[j], static_cast<uint32_t>(kt * 128));
-        }
+        const bool past = kt == nk - 1 && along_chunk(along_row(j, BY / 4)) >= tail;
+        dma_load16(at, rsrc_y0, past ? kNoRowOffset : vy[j], static_cast<uint32_t>(kt * 128));
     };
 
-    const int wy = wave >> 1, wx = wave & 1;
+    const int wy = wave / WX, wx = wave % WX;
     const int r32 = lane & 31, half = lane >> 5;
     int valid_blocks = 0;
 #pragma unroll
-    for (int m = 0; m < YB; ++m) valid_blocks += (wy + 2 * m) < nblk;
+    for (int m = 0; m < YB; ++m) valid_blocks += (wy + WY * m) < nblk;
 
     Acc acc[YB][XB];
 #pragma unroll
@@ -289,8 +237,8 @@ __global__ __launch_bounds__(kThreads, (TileShape<MODE, I8, BX, BY, GATHER>::kPe
         return v;
     };
 
-    // stages [s0, s1) with NV valid row blocks in this wave
-    auto k_loop = [&](auto nv_tag, const int s0, const int s1) {
+    // the stages, with NV valid row blocks in this wave
+    auto k_loop = [&](auto nv_tag) {
         constexpr int NV = decltype(nv_tag)::value;
         constexpr int NA = NV > 0 ? NV : 1;
         constexpr int MF = NV * XB;  // matrix instructions per substep
@@ -302,10 +250,7 @@ __global__ __launch_bounds__(kThreads, (TileShape<MODE, I8, BX, BY, GATHER>::kPe
         auto load_piece = [&](Frags& f, int yb, int xb, int ks, auto qc) {
             constexpr int q = decltype(qc)::value;
             if constexpr (q < NV) {
-                if constexpr (TRY)
-                    f.y[q] = read_down(y_buf(yb), BY, wy + 2 * q, ks);
-                else
-                    f.y[q] = read_along(y_buf(yb), wy + 2 * q, ks);
+                f.y[q] = read_along(y_buf(yb), wy + WY * q, ks);
             } else if constexpr (NV > 0) {
                 constexpr int n = q - NV;
                 if constexpr (TRX)
@@ -328,43 +273,41 @@ __global__ __launch_bounds__(kThreads, (TileShape<MODE, I8, BX, BY, GATHER>::kPe
             }
         };
         const int last = s1 - 1;
-        // prologue: Y(0), X(0) and with three buffers X(1) in flight
-        load_index(s0);
+        static_for<0, XA>([&](auto sc) {
+            constexpr int st = decltype(sc)::value;
+            if constexpr (st < YA) {
 #pragma unroll
-        for (int j = 0; j < DMA_Y; ++j) dma_y(j, 0, s0);
+                for (int j = 0; j < DMA_Y; ++j) dma_y(j, st, min(s0 + st, last));
+            }
 #pragma unroll
-        for (int j = 0; j < DMA_X; ++j) dma_x(j, 0, s0);
-        if constexpr (XBUFS == 3) {
-#pragma unroll
-            for (int j = 0; j < DMA_X; ++j) dma_x(j, 1, min(s0 + 1, last));
-            wait_vmcnt<DMA_X>();
-        } else {
-            wait_vmcnt<0>();
-        }
+            for (int j = 0; j < DMA_X; ++j) dma_x(j, st, min(s0 + st, last));
+        });
+        wait_vmcnt<YOUNGER>();
         __syncthreads();
         int ybuf = 0, xbuf = 0;
         Frags f0, f1;
         load_frags(f0, 0, 0, 0);
         for (int kt = s0; kt < s1; ++kt) {
             // past the end: an idle buffer is filled again
-            const int ky = min(kt + 1, last);
-            const int kx = min(kt + XBUFS - 1, last);
-            const int ynext = ybuf ^ 1;
-            const int xnext = XBUFS == 3 ? (xbuf == 0 ? 2 : xbuf - 1) : xbuf ^ 1;
-            load_index(kx);
+            const int ky = min(kt + YA, last);
+            const int kx = min(kt + XA, last);
+            const int ynext = ybuf == 0 ? YBUFS - 1 : ybuf - 1;  // the buffer freed last
+            const int xnext = xbuf == 0 ? XBUFS - 1 : xbuf - 1;
             // The stage's loads are spread over the matrix instructions of its
             // four substeps, the reads of the next substep's operands between
             // them (scheduling fences keep them there).  The barrier sits
             // before the last eighth of the last substep, so the first
             // operands of the next stage are read while those run.
-            constexpr int LPS = (DMA_X + DMA_Y) / 4;
-            static_assert(LPS * 4 == DMA_X + DMA_Y, "loads split evenly over the substeps");
+            constexpr int LOADS = DMA_X + DMA_Y;
             auto substep = [&](const Frags& f, auto sc, auto lo_c, auto hi_c, Frags& fn, auto kn_c) {
                 constexpr int sub = decltype(sc)::value;
                 constexpr int LO = decltype(lo_c)::value, HI = decltype(hi_c)::value;
                 constexpr int KN = decltype(kn_c)::value;
                 constexpr int NM = HI - LO;
-                constexpr int NL = sub >= 0 ? LPS : 0;
+                // this substep's loads: [L0, L1) of the stage's
+                constexpr int L0 = sub >= 0 ? (sub * LOADS + 3) / 4 : 0;
+                constexpr int L1 = sub >= 0 ? ((sub + 1) * LOADS + 3) / 4 : 0;
+                constexpr int NL = L1 - L0;
                 constexpr int NPC = KN >= 0 ? NP : 0;
                 constexpr int IT0 = NM > NL ? NM : NL;
                 constexpr int IT = IT0 > 0 ? IT0 : 1;
@@ -377,7 +320,7 @@ __global__ __launch_bounds__(kThreads, (TileShape<MODE, I8, BX, BY, GATHER>::kPe
                     if constexpr (i < NM) mfma_one(f, std::integral_constant<int, LO + i>{});
                     constexpr int step = NM >= NL ? (NL > 0 ? NM / NL : 1) : 1;
                     if constexpr (NL > 0 && i % step == step - 1 && i / step < NL) {
-                        constexpr int j = sub * LPS + i / step;
+                        constexpr int j = L0 + i / step;
                         if constexpr (j < DMA_Y)
                             dma_y(j, ynext, ky);
                         else
@@ -398,10 +341,10 @@ __global__ __launch_bounds__(kThreads, (TileShape<MODE, I8, BX, BY, GATHER>::kPe
             substep(f1, K1{}, C0{}, CM{}, f0, K2{});
             substep(f0, K2{}, C0{}, CM{}, f1, K3{});
             substep(f1, K3{}, C0{}, CH{}, f0, KNone{});
-            wait_vmcnt<XBUFS == 3 ? DMA_X : 0>();
+            wait_vmcnt<YOUNGER>();
             __syncthreads();
-            ybuf = ynext;
-            xbuf = XBUFS == 3 ? (xbuf == 2 ? 0 : xbuf + 1) : xnext;
+            ybuf = ybuf == YBUFS - 1 ? 0 : ybuf + 1;
+            xbuf = xbuf == XBUFS - 1 ? 0 : xbuf + 1;
             load_frags(f0, ybuf, xbuf, 0);  // after the last stage: read, never used
             __builtin_amdgcn_sched_barrier(0);
             substep(f1, KNone{}, CH{}, CM{}, f0, KNone{});
@@ -409,45 +352,9 @@ __global__ __launch_bounds__(kThreads, (TileShape<MODE, I8, BX, BY, GATHER>::kPe
         wait_vmcnt<0>();
         __syncthreads();
     };
-    auto run_stages = [&](int s0, int s1) {
-        if constexpr (MODE == kWeightGrad) {
-            k_loop(std::integral_constant<int, YB>{}, s0, s1);
-        } else if constexpr (YB == 4) {
-            switch (valid_blocks) {
-                case 0: k_loop(std::integral_constant<int, 0>{}, s0, s1); break;
-                case 1: k_loop(std::integral_constant<int, 1>{}, s0, s1); break;
-                case 2: k_loop(std::integral_constant<int, 2>{}, s0, s1); break;
-                case 3: k_loop(std::integral_constant<int, 3>{}, s0, s1); break;
-                default: k_loop(std::integral_constant<int, YB>{}, s0, s1); break;
-            }
-        } else {
-            switch (valid_blocks) {
-                case 0: k_loop(std::integral_constant<int, 0>{}, s0, s1); break;
-                case 1: k_loop(std::integral_constant<int, 1>{}, s0, s1); break;
-                default: k_loop(std::integral_constant<int, YB>{}, s0, s1); break;
-            }
-        }
-    };
-    if constexpr (INDEX) {
-        for (stage0 = 0; stage0 < nk; stage0 += kGatherRows / SK) {
-            // byte offsets of the rows of the next stages; past the last row,
-            // an offset past the buffer
-            const int q0 = stage0 * SK;
-            for (int i = tid; i < kGatherRows; i += kThreads) {
-                uint32_t off = kNoRowOffset;
-                if (q0 + i < red) {
-                    int64_t s = g.pairs[first + q0 + i] / g.k;
-                    s = s < 0 ? 0 : (s >= g.S ? g.S - 1 : s);
-                    off = static_cast<uint32_t>(s * K * 2);
-                }
-                if (i < (nk - stage0) * SK) s_index[i] = off;
-            }
-            __syncthreads();
-            run_stages(stage0, min(nk, stage0 + kGatherRows / SK));
-        }
-    } else if (nk > 0) {
-        run_stages(0, nk);
-    }
+    static_for<0, YB + 1>([&](auto nv_tag) {
+        if (valid_blocks == decltype(nv_tag)::value) k_loop(nv_tag);
+    });
 
     // ---- epilogue: through LDS, one block of 32 rows of this wave at a time
     // (a region of its own, so no barrier), so that the stores are 16 bytes a
@@ -459,10 +366,13 @@ __global__ __launch_bounds__(kThreads, (TileShape<MODE, I8, BX, BY, GATHER>::kPe
     static_assert(4 * REGION <= Shape::kArena, "epilogue region");
     unsigned char* region = s_arena + wave * REGION;
     const int wc0 = c0 + wx * WCOLS;
+    const bool out_bf16 = g.out_bf16 && !split, accumulate = g.accumulate && !split;
+    void* const out =
+        split ? static_cast<float*>(g.ws) + static_cast<int64_t>(blockIdx.y) * g.P * cols : static_cast<float*>(g.out);
 #pragma unroll
     for (int m = 0; m < YB; ++m) {
         if (m >= valid_blocks) continue;
-        const int blk = wy + 2 * m;
+        const int blk = wy + WY * m;
         float a_sc = 0.0f;
         if constexpr (I8) {
             const int64_t q = orow0 + min(blk * 32 + r32, rows - 1);
@@ -476,7 +386,13 @@ __global__ __launch_bounds__(kThreads, (TileShape<MODE, I8, BX, BY, GATHER>::kPe
             for (int i4 = 0; i4 < 4; ++i4) {
                 const int col = n * 32 + 8 * i4 + 4 * half;
                 f32x4 v;
-                if constexpr (I8) {
+                if (split) {  // raw sums
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const auto x = acc[m][n][4 * i4 + i];
+                        v[i] = __builtin_bit_cast(float, x);
+                    }
+                } else if constexpr (I8) {
                     const int at = min(wc0 + col, cols - 4);
                     const f32x4 ws = *reinterpret_cast<const f32x4*>(g.w_scale + static_cast<int64_t>(e) * N + at);
 #pragma unroll
@@ -485,7 +401,7 @@ __global__ __launch_bounds__(kThreads, (TileShape<MODE, I8, BX, BY, GATHER>::kPe
 #pragma unroll
                     for (int i = 0; i < 4; ++i) v[i] = acc[m][n][4 * i4 + i];
                 }
-                if (g.out_bf16) {
+                if (out_bf16) {
                     u32x2 h;
                     h[0] = pack_bf16(v[0], v[1]);
                     h[1] = pack_bf16(v[2], v[3]);
@@ -497,14 +413,14 @@ __global__ __launch_bounds__(kThreads, (TileShape<MODE, I8, BX, BY, GATHER>::kPe
         wave_lds_fence();
         const int64_t base = (orow0 + blk * 32) * cols + wc0;
         const int left = rows - blk * 32;  // rows of this block inside the tile
-        if (g.out_bf16) {
+        if (out_bf16) {
             constexpr int LPR = WCOLS / 8;  // lanes per row
 #pragma unroll
             for (int it = 0; it < 32 * LPR / 64; ++it) {
                 const int r = it * (64 / LPR) + lane / LPR, c = lane % LPR * 8;
                 const u32x4 v = ld16(region + r * (WCOLS * 2 + 16) + c * 2);
                 if (r < left && wc0 + c < cols)
-                    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(g.out) + base + static_cast<int64_t>(r) * cols + c) = v;
+                    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + base + static_cast<int64_t>(r) * cols + c) = v;
             }
         } else {
             constexpr int LPR = WCOLS / 4;
@@ -513,8 +429,8 @@ __global__ __launch_bounds__(kThreads, (TileShape<MODE, I8, BX, BY, GATHER>::kPe
                 const int r = it * (64 / LPR) + lane / LPR, c = lane % LPR * 4;
                 f32x4 v = *reinterpret_cast<const f32x4*>(region + r * PITCH + c * 4);
                 if (r < left && wc0 + c < cols) {
-                    f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + base + static_cast<int64_t>(r) * cols + c);
-                    if (g.accumulate) v += *o;
+                    f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(out) + base + static_cast<int64_t>(r) * cols + c);
+                    if (accumulate) v += *o;
                     *o = v;
                 }
             }

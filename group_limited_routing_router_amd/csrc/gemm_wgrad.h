@@ -32,13 +32,6 @@ namespace {
 
 constexpr int kNumCu = 256;
 
-// A tile of the weight gradient: expert, first output column and row, and the
-// expert's positions [first, first + red).
-struct WgradTile {
-    int e, c0, n0, red, nk;
-    int64_t first;
-};
-
 template <int BX, int BY, bool GATHER>
 struct WgradShape {
     static constexpr int kRows = 32;  // positions per stage
@@ -78,24 +71,36 @@ __global__ __launch_bounds__(kThreads, (WgradShape<BX, BY, GATHER>::kPerCu)) voi
     const int col_tiles = (K + BX - 1) / BX, row_tiles = (N + BY - 1) / BY;
     const int per_expert = col_tiles * row_tiles;
     const int xcd = blockIdx.x % kNumXcd, slots = gridDim.x / kNumXcd;
-    const bool interleave = g.E % kNumXcd == 0;
+    // With splits > 1 the positions of an expert come in that many parts, each
+    // a list entry of its own whose output is the part's own array (part s of
+    // expert e: array s * E + e of out).
+    const int parts = g.E * g.splits;
+    const bool interleave = parts % kNumXcd == 0;
     auto expert_at = [&](int pos) {
-        return interleave ? (pos % kNumXcd) * (g.E / kNumXcd) + pos / kNumXcd : pos;
+        return interleave ? (pos % kNumXcd) * (parts / kNumXcd) + pos / kNumXcd : pos;
+    };
+    auto part_of = [&](int e, int64_t& b, int64_t& n) {  // positions of part e / E, from the expert's
+        if (g.splits > 1) {
+            const int64_t each = (n + g.splits * SR - 1) / (g.splits * SR) * SR, skip = each * (e / g.E);
+            b += skip < n ? skip : n;
+            n = skip < n ? (n - skip < each ? n - skip : each) : 0;
+        }
     };
     typedef const __attribute__((address_space(4))) int32_t* ConstInts;
     auto expert_span = [&](int e, int64_t& b, int64_t& m) {
         b = 0;
         m = g.P;
         if (g.offsets) {
-            b = g.offsets[e];
-            m = g.offsets[e + 1];
+            b = g.offsets[e % g.E];
+            m = g.offsets[e % g.E + 1];
             b = b < 0 ? 0 : (b > g.P ? g.P : b);
             m = m < 0 ? 0 : (m > g.P ? g.P : m);
         }
         m = m > b ? m - b : 0;
+        part_of(e, b, m);
     };
     int l0, run_end;
-    const int total = per_expert * g.E;
+    const int total = per_expert * parts;
     if (total <= static_cast<int>(gridDim.x)) {  // one tile a workgroup
         const int per = total / kNumXcd, rem = total % kNumXcd;
         const int begin = xcd * per + min(xcd, rem);
@@ -106,7 +111,7 @@ __global__ __launch_bounds__(kThreads, (WgradShape<BX, BY, GATHER>::kPerCu)) voi
         int* s_bound = reinterpret_cast<int*>(s_arena + kWaves * 8);     // [kNumXcd + 1]
         constexpr int kTileCost = BF16 ? 8 : 16;
         int64_t cost = 0;
-        if (tid < g.E) {
+        if (tid < parts) {
             int64_t b, n;
             expert_span(expert_at(tid), b, n);
             cost = (n + SR - 1) / SR + kTileCost;
@@ -130,36 +135,63 @@ __global__ __launch_bounds__(kThreads, (WgradShape<BX, BY, GATHER>::kPerCu)) voi
         const int64_t end = incl * per_expert, begin = end - cost * per_expert;
         for (int x = 0; x <= kNumXcd; ++x) {
             const int64_t at = all * x / kNumXcd;
-            if (tid < g.E && at >= begin && at < end)
+            if (tid < parts && at >= begin && at < end)
                 s_bound[x] = tid * per_expert + static_cast<int>((at - begin + cost - 1) / cost);
         }
-        if (tid == 0) s_bound[kNumXcd] = per_expert * g.E;
+        if (tid == 0) s_bound[kNumXcd] = total;
         __syncthreads();
         l0 = __builtin_amdgcn_readfirstlane(s_bound[xcd]) + blockIdx.x / kNumXcd;
         run_end = __builtin_amdgcn_readfirstlane(s_bound[xcd + 1]);
         __syncthreads();  // before the loads reuse this part of LDS
     }
-    auto tile_at = [&](int l) {
-        WgradTile t;
-        const int pos = l / per_expert, in = l - pos * per_expert;
-        t.e = expert_at(pos);
-        const int band = in / (kBand * col_tiles), ib = in - band * kBand * col_tiles;
-        const int high = min(kBand, row_tiles - band * kBand);
-        const int ct = ib / high;
-        t.c0 = ct * BX;
-        t.n0 = (band * kBand + ib - ct * high) * BY;
+    // A place in this workgroup's stages: tile `l` of the list (tile `in` of
+    // the expert at position pos), its stage k.  Steps go from the tile before,
+    // without divisions, and read the offsets only where the expert changes.
+    struct Cursor {
+        int l, pos, in, k;
+        int e, red, nk;  // expert, its positions [first, first + red), stages
+        int64_t first;
+        int c0, n0;      // first output column and row
+    };
+    auto enter_expert = [&](Cursor& c) {
+        c.e = expert_at(c.pos);
         int64_t b = 0, m = g.P;
         if (g.offsets) {
             const ConstInts off = (ConstInts)g.offsets;
-            b = off[t.e];
-            m = off[t.e + 1];
+            const int e = g.splits > 1 ? c.e % g.E : c.e;
+            b = off[e];
+            m = off[e + 1];
             b = b < 0 ? 0 : (b > g.P ? g.P : b);
             m = m < 0 ? 0 : (m > g.P ? g.P : m);
         }
-        t.first = b;
-        t.red = static_cast<int>(m > b ? m - b : 0);
-        t.nk = (t.red + SR - 1) / SR;
-        return t;
+        m = m > b ? m - b : 0;
+        part_of(c.e, b, m);
+        // the same in every lane (P < 2^31): kept in scalar registers
+        c.first = __builtin_amdgcn_readfirstlane(static_cast<int>(b));
+        c.red = __builtin_amdgcn_readfirstlane(static_cast<int>(m));
+        c.nk = (c.red + SR - 1) / SR;
+    };
+    auto enter_tile = [&](Cursor& c) {
+        const int band_tiles = kBand * col_tiles;
+        const int band = row_tiles > kBand ? c.in / band_tiles : 0;
+        const int ib = c.in - band * band_tiles;
+        const int high = min(kBand, row_tiles - band * kBand);
+        const int ct = high == kBand ? ib / kBand : ib / high;
+        c.c0 = ct * BX;
+        c.n0 = (band * kBand + ib - ct * high) * BY;
+        c.k = 0;
+    };
+    auto step = [&](Cursor& c) {  // to the next tile, which has to be in the run
+        c.l += slots;
+        c.in += slots;
+        if (c.in >= per_expert) {
+            do {
+                c.in -= per_expert;
+                ++c.pos;
+            } while (c.in >= per_expert);
+            enter_expert(c);
+        }
+        enter_tile(c);
     };
     if (l0 >= run_end) return;
 
@@ -177,34 +209,32 @@ __global__ __launch_bounds__(kThreads, (WgradShape<BX, BY, GATHER>::kPerCu)) voi
         const int r = down_row(j, BY / 8);
         vy[j] = static_cast<uint32_t>(r * N * 2 + ((lane % (BY / 8)) ^ tr_swizzle(r)) * 16);
     }
-    // A place in this workgroup's stages: tile (list index l), its stage k.
-    // Past the last stage it stays there (an idle buffer is filled again).
-    struct Cursor {
-        WgradTile t;
-        int l, k;
-    };
-    auto next_filled = [&](Cursor& c) {  // from list index c.l on, the first tile with rows
-        while (c.t.nk == 0) {
+    auto next_filled = [&](Cursor& c) {  // from tile c on, the first with rows
+        while (c.nk == 0) {
             if (c.l + slots >= run_end) return false;
-            c.l += slots;
-            c.t = tile_at(c.l);
+            step(c);
         }
         return true;
     };
+    // past the last stage a cursor stays there (an idle buffer is filled again)
     auto advance = [&](Cursor& c) {
-        if (c.k + 1 < c.t.nk) {
+        if (c.k + 1 < c.nk) {
             ++c.k;
             return;
         }
         Cursor n = c;
         if (n.l + slots < run_end) {
-            n.l += slots;
-            n.t = tile_at(n.l);
-            n.k = 0;
+            step(n);
             if (next_filled(n)) c = n;
         }
     };
-    Cursor ld{tile_at(l0), l0, 0};  // the stage loaded next
+    Cursor now;  // the tile computed
+    now.l = l0;
+    now.pos = l0 / per_expert;
+    now.in = l0 - now.pos * per_expert;
+    enter_expert(now);
+    enter_tile(now);
+    Cursor ld = now;  // the stage loaded next
     const bool any = next_filled(ld);
     // GATHER: the row indexes of a stage come into LDS AHEAD stages before
     // the stage's own loads, each wave its own copy (pairs of the 32
@@ -215,7 +245,7 @@ __global__ __launch_bounds__(kThreads, (WgradShape<BX, BY, GATHER>::kPerCu)) voi
     const uint32_t index_at = arena + NBUF * STAGE + wave * (Shape::kSlots * 256);
     auto dma_index = [&]() {
         if constexpr (GATHER) {
-            const int64_t at = ix.t.first + ix.k * SR;
+            const int64_t at = ix.first + ix.k * SR;
             const int64_t left = g.P - at < 64 ? g.P - at : 64;
             asm volatile(
                 "s_mov_b32 m0, %0\n\t"
@@ -235,7 +265,7 @@ __global__ __launch_bounds__(kThreads, (WgradShape<BX, BY, GATHER>::kPerCu)) voi
     auto read_index = [&]() {
         if constexpr (GATHER) {
             const int32_t* idx = reinterpret_cast<const int32_t*>(s_arena + (index_at - arena) + ld_slot * 256);
-            const int valid = min(SR, ld.t.red - ld.k * SR);
+            const int valid = min(SR, ld.red - ld.k * SR);
 #pragma unroll
             for (int j = 0; j < DMA_X; ++j) {
                 const int r = down_row(j, BX / 8);
@@ -253,22 +283,22 @@ __global__ __launch_bounds__(kThreads, (WgradShape<BX, BY, GATHER>::kPerCu)) voi
     };
     auto dma_x = [&](int j, uint32_t buf) {
         const uint32_t at = buf + wave * (XS / 4) + j * 1024;
-        const unsigned char* a = static_cast<const unsigned char*>(g.a) + static_cast<int64_t>(ld.t.c0) * 2;
-        const int valid = min(SR, ld.t.red - ld.k * SR);
+        const unsigned char* a = static_cast<const unsigned char*>(g.a) + static_cast<int64_t>(ld.c0) * 2;
+        const int valid = min(SR, ld.red - ld.k * SR);
         if constexpr (GATHER) {
-            dma_load16(at, make_rsrc(a, static_cast<uint32_t>((g.S * K - ld.t.c0) * 2)), src[j] + vx[j], 0);
+            dma_load16(at, make_rsrc(a, static_cast<uint32_t>((g.S * K - ld.c0) * 2)), src[j] + vx[j], 0);
         } else {
-            dma_load16(at, make_rsrc(a + (ld.t.first + ld.k * SR) * K * 2,
-                                     static_cast<uint32_t>((valid * K - ld.t.c0) * 2)),
+            dma_load16(at, make_rsrc(a + (ld.first + ld.k * SR) * K * 2,
+                                     static_cast<uint32_t>((valid * K - ld.c0) * 2)),
                        vx[j], 0);
         }
     };
     auto dma_y = [&](int j, uint32_t buf) {
-        const int valid = min(SR, ld.t.red - ld.k * SR);
+        const int valid = min(SR, ld.red - ld.k * SR);
         dma_load16(buf + XS + wave * (YS / 4) + j * 1024,
                    make_rsrc(static_cast<const unsigned char*>(g.dout) +
-                                 ((ld.t.first + ld.k * SR) * N + ld.t.n0) * 2,
-                             static_cast<uint32_t>((valid * N - ld.t.n0) * 2)),
+                                 ((ld.first + ld.k * SR) * N + ld.n0) * 2,
+                             static_cast<uint32_t>((valid * N - ld.n0) * 2)),
                    vy[j], 0);
     };
 
@@ -313,10 +343,16 @@ __global__ __launch_bounds__(kThreads, (WgradShape<BX, BY, GATHER>::kPerCu)) voi
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.0f;
     };
-    auto mfma_one = [&](const Frags& f, auto ic) {
+    // onto_zero: a tile's first products
+    auto mfma_one = [&](const Frags& f, auto ic, auto onto_zero) {
         constexpr int i = decltype(ic)::value;
         constexpr int m = i % YB, n = i / YB;
-        acc[m][n] = mfma32(as_bf16x8(f.x[n]), as_bf16x8(f.y[m]), acc[m][n]);
+        if constexpr (decltype(onto_zero)::value) {
+            const f32x16 zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            acc[m][n] = mfma32(as_bf16x8(f.x[n]), as_bf16x8(f.y[m]), zero);
+        } else {
+            acc[m][n] = mfma32(as_bf16x8(f.x[n]), as_bf16x8(f.y[m]), acc[m][n]);
+        }
     };
 
     Frags f0, f1;
@@ -348,17 +384,18 @@ __global__ __launch_bounds__(kThreads, (WgradShape<BX, BY, GATHER>::kPerCu)) voi
     constexpr int RELAXED = (AHEAD - 1) * DMA + STORES < 63 ? (AHEAD - 1) * DMA + STORES : 63;
     int since = AHEAD;  // stages since the last stores
 
-    for (int l = l0; l < run_end; l += slots) {
-        const WgradTile t = tile_at(l);
-        clear();
-        for (int kt = 0; kt < t.nk; ++kt) {
+    while (true) {
+        const Cursor t = now;
+        auto stage = [&](auto first_c) {
+            constexpr bool FIRST = decltype(first_c)::value;
             const uint32_t buf = place(cur);
             const uint32_t into = place(cur == 0 ? NBUF - 1 : cur - 1);
             read_index();
             dma_index();
             // two substeps; the stage's loads and the next operands' reads
             // spread over their matrix instructions
-            auto substep = [&](const Frags& f, auto lo_c, auto hi_c, auto first_load, auto num_loads, auto reads) {
+            auto substep = [&](const Frags& f, auto lo_c, auto hi_c, auto first_load, auto num_loads, auto reads,
+                               auto onto_zero) {
                 constexpr int LO = decltype(lo_c)::value, HI = decltype(hi_c)::value;
                 constexpr int L0 = decltype(first_load)::value, NL = decltype(num_loads)::value;
                 constexpr int NPC = decltype(reads)::value ? NP : 0;
@@ -369,7 +406,7 @@ __global__ __launch_bounds__(kThreads, (WgradShape<BX, BY, GATHER>::kPerCu)) voi
                         constexpr int q = decltype(qc)::value;
                         if constexpr (q * NM / NP == i) load_piece(f1, buf, 1, qc);
                     });
-                    mfma_one(f, std::integral_constant<int, LO + i>{});
+                    mfma_one(f, std::integral_constant<int, LO + i>{}, onto_zero);
                     static_for<0, NL>([&](auto jc) {
                         constexpr int j = decltype(jc)::value;
                         if constexpr ((j + 1) * NM / NL - 1 == i || (NM < NL && j * NM / NL == i)) {
@@ -388,8 +425,8 @@ __global__ __launch_bounds__(kThreads, (WgradShape<BX, BY, GATHER>::kPerCu)) voi
             using CH = std::integral_constant<int, MF * 3 / 4>;
             using LY = std::integral_constant<int, DMA_Y>;
             using LX = std::integral_constant<int, DMA_X>;
-            substep(f0, C0{}, CM{}, C0{}, LY{}, std::true_type{});
-            substep(f1, C0{}, CH{}, LY{}, LX{}, std::false_type{});
+            substep(f0, C0{}, CM{}, C0{}, LY{}, std::true_type{}, std::integral_constant<bool, FIRST>{});
+            substep(f1, C0{}, CH{}, LY{}, LX{}, std::false_type{}, std::false_type{});
             ld_next();
             if (since < AHEAD - 1)
                 wait_vmcnt<RELAXED>();
@@ -400,9 +437,14 @@ __global__ __launch_bounds__(kThreads, (WgradShape<BX, BY, GATHER>::kPerCu)) voi
             cur = cur == NBUF - 1 ? 0 : cur + 1;
             static_for<0, NP>([&](auto qc) { load_piece(f0, place(cur), 0, qc); });
             __builtin_amdgcn_sched_barrier(0);
-            substep(f1, CH{}, CM{}, C0{}, C0{}, std::false_type{});
+            substep(f1, CH{}, CM{}, C0{}, C0{}, std::false_type{}, std::false_type{});
+        };
+        if (t.nk > 0) {
+            stage(std::true_type{});
+            for (int kt = 1; kt < t.nk; ++kt) stage(std::false_type{});
+        } else {
+            clear();
         }
-        if (ACC && t.nk == 0) continue;
 
         // ---- write the tile: 32 rows x PITCH bytes at a time through this
         // wave's part of the idle buffer, X's and Y's in turn ----
@@ -421,56 +463,75 @@ __global__ __launch_bounds__(kThreads, (WgradShape<BX, BY, GATHER>::kPerCu)) voi
         auto chunk_at = [&](int r, int c) {
             return r * PITCH + ((c ^ (CPR == 8 ? (r >> 1) & 7 : (r >> 2) & 3)) << 4);
         };
-        static_for<0, YB>([&](auto mc) {
-            constexpr int m = decltype(mc)::value;
-            static_for<0, PASSES>([&](auto pc) {
-                constexpr int p = decltype(pc)::value;
-                unsigned char* region = s_arena + (idle - arena) +
-                                        ((m * PASSES + p) & 1 ? XS + wave * (YS / 4) : wave * (XS / 4));
-                static_for<0, PASS_COLS / 16>([&](auto cc) {
-                    // 16 columns: this lane's 8 (chunks of 16 bytes: one of
-                    // bf16, two of fp32)
-                    constexpr int c16 = decltype(cc)::value;
-                    constexpr int col = p * PASS_COLS + c16 * 16;
-                    constexpr int n = col / 32, i0 = (col % 32) / 2;
-                    const f32x16 v = acc[m][n];
-                    if constexpr (BF16) {
-                        u32x4 h;
+        constexpr int UNITS = YB * PASSES, PER_UNIT = 32 * CPR / 64;
+        auto region = [&](int u) {
+            return s_arena + (idle - arena) + (u & 1 ? XS + wave * (YS / 4) : wave * (XS / 4));
+        };
+        auto put = [&](auto uc) {
+            constexpr int u = decltype(uc)::value, m = u / PASSES, p = u % PASSES;
+            static_for<0, PASS_COLS / 16>([&](auto cc) {
+                // 16 columns: this lane's 8 (chunks of 16 bytes: one of bf16,
+                // two of fp32)
+                constexpr int c16 = decltype(cc)::value;
+                constexpr int col = p * PASS_COLS + c16 * 16;
+                constexpr int n = col / 32, i0 = (col % 32) / 2;
+                const f32x16 v = acc[m][n];
+                if constexpr (BF16) {
+                    u32x4 h;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) h[i] = pack_bf16(v[i0 + 2 * i], v[i0 + 2 * i + 1]);
-                        *reinterpret_cast<u32x4*>(region + chunk_at(r32, c16 * 2 + half)) = h;
-                    } else {
+                    for (int i = 0; i < 4; ++i) h[i] = pack_bf16(v[i0 + 2 * i], v[i0 + 2 * i + 1]);
+                    *reinterpret_cast<u32x4*>(region(u) + chunk_at(r32, c16 * 2 + half)) = h;
+                } else {
 #pragma unroll
-                        for (int d = 0; d < 2; ++d) {
-                            f32x4 h;
+                    for (int d = 0; d < 2; ++d) {
+                        f32x4 h;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) h[i] = v[i0 + 4 * d + i];
-                            *reinterpret_cast<f32x4*>(region + chunk_at(r32, c16 * 4 + half * 2 + d)) = h;
-                        }
-                    }
-                });
-                wave_lds_fence();
-#pragma unroll
-                for (int it = 0; it < 32 * CPR / 64; ++it) {
-                    const int r = it * (64 / CPR) + lane / CPR, c = lane % CPR;
-                    u32x4 v = ld16(region + chunk_at(r, c));
-                    const int orow = (wy * YB + m) * 32 + r;
-                    const int ocol = wx * XB * 32 + p * PASS_COLS + c * (16 / OB);
-                    const bool in = orow < rows && ocol < cols;
-                    const uint32_t off = static_cast<uint32_t>((orow * static_cast<int64_t>(K) + ocol) * OB);
-                    if constexpr (ACC) {
-                        if (in) {
-                            f32x4* o = reinterpret_cast<f32x4*>(static_cast<unsigned char*>(g.out) + at0 + off);
-                            *o = *o + __builtin_bit_cast(f32x4, v);
-                        }
-                    } else {
-                        __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, in ? off : kNoRowOffset, 0, 0);
+                        for (int i = 0; i < 4; ++i) h[i] = v[i0 + 4 * d + i];
+                        *reinterpret_cast<f32x4*>(region(u) + chunk_at(r32, c16 * 4 + half * 2 + d)) = h;
                     }
                 }
-                wave_lds_fence();
             });
+        };
+        u32x4 v[2][PER_UNIT];
+        auto fetch = [&](auto uc) {
+            constexpr int u = decltype(uc)::value;
+#pragma unroll
+            for (int it = 0; it < PER_UNIT; ++it)
+                v[u & 1][it] = ld16(region(u) + chunk_at(it * (64 / CPR) + lane / CPR, lane % CPR));
+        };
+        const int64_t row_bytes = static_cast<int64_t>(K) * OB;
+        auto send = [&](auto uc) {
+            constexpr int u = decltype(uc)::value, m = u / PASSES, p = u % PASSES;
+            const int ocol = wx * XB * 32 + p * PASS_COLS + lane % CPR * (16 / OB);
+#pragma unroll
+            for (int it = 0; it < PER_UNIT; ++it) {
+                const int orow = (wy * YB + m) * 32 + it * (64 / CPR) + lane / CPR;
+                const bool in = orow < rows && ocol < cols;
+                const uint32_t off = static_cast<uint32_t>(orow * row_bytes + ocol * OB);
+                if constexpr (ACC) {
+                    if (in && t.nk > 0) {
+                        f32x4* o = reinterpret_cast<f32x4*>(static_cast<unsigned char*>(g.out) + at0 + off);
+                        *o = *o + __builtin_bit_cast(f32x4, v[u & 1][it]);
+                    }
+                } else {
+                    __builtin_amdgcn_raw_buffer_store_b128(v[u & 1][it], rsrc, in ? off : kNoRowOffset, 0, 0);
+                }
+            }
+        };
+        // unit u + 1 goes into LDS while unit u comes back
+        put(std::integral_constant<int, 0>{});
+        static_for<0, UNITS>([&](auto uc) {
+            constexpr int u = decltype(uc)::value;
+            wave_lds_fence();
+            if constexpr (u + 1 < UNITS) put(std::integral_constant<int, u + 1>{});
+            fetch(uc);
+            wave_lds_fence();
+            if constexpr (u > 0) send(std::integral_constant<int, u - 1>{});
         });
+        send(std::integral_constant<int, UNITS - 1>{});
         since = 0;
+        if (now.l + slots >= run_end) break;
+        step(now);
     }
     wait_vmcnt<0>();
 }

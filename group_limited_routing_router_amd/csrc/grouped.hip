@@ -163,31 +163,173 @@ hipError_t launch_plain(const GemmArgs& g, hipStream_t s) {
 template <int MODE, int BX, int BY>
 int64_t tile_grid(const GemmArgs& g) {
     const int64_t cols = MODE == kProduct ? g.N : g.K;
-    const int64_t row_tiles = MODE == kWeightGrad ? static_cast<int64_t>((g.N + BY - 1) / BY) * g.E
-                                                  : (g.P + BY - 1) / BY + (g.E < g.P ? g.E : g.P);
+    const int64_t row_tiles = (g.P + BY - 1) / BY + (g.E < g.P ? g.E : g.P);
     const int64_t tiles = row_tiles * ((cols + BX - 1) / BX);
     return (tiles + kNumXcd - 1) / kNumXcd * kNumXcd;
 }
 
-template <int MODE, bool I8, int BX, int BY>
-hipError_t launch_tiles(const GemmArgs& g, hipStream_t s) {
+// splits > 1: the reduction in that many parts, whose sums go to g.ws.
+template <int MODE, bool I8, int BX, int BY, bool NT = false>
+hipError_t launch_tiles(const GemmArgs& g, hipStream_t s, int splits = 1) {
     const int64_t grid = tile_grid<MODE, BX, BY>(g);
     if (grid <= 0) return hipSuccess;
     if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-    const dim3 blocks(static_cast<unsigned>(grid)), threads(kThreads);
-    if constexpr (MODE != kInputGrad) {
+    const dim3 blocks(static_cast<unsigned>(grid), splits), threads(kThreads);
+    if constexpr (MODE == kProduct) {
         if (g.pairs) {
-            gemm_tile_kernel<MODE, I8, BX, BY, true><<<blocks, threads, 0, s>>>(g);
+            gemm_tile_kernel<MODE, I8, BX, BY, true, NT><<<blocks, threads, 0, s>>>(g);
             return hipGetLastError();
         }
     }
-    gemm_tile_kernel<MODE, I8, BX, BY, false><<<blocks, threads, 0, s>>>(g);
+    gemm_tile_kernel<MODE, I8, BX, BY, false, NT><<<blocks, threads, 0, s>>>(g);
     return hipGetLastError();
 }
 
+// The gathered rows of a, addressed with 32-bit offsets by the tiled kernels.
+bool gather_fits(const GemmArgs& g, int bytes) {
+    return !g.pairs || g.S * static_cast<int64_t>(g.K) * bytes <= static_cast<int64_t>(kNoRowOffset);
+}
+
+// How the product and the input gradient of a shape run.
+struct TilePlan {
+    int rows;    // tile: 32 x 128, 128 x 128 or 256 x 256
+    bool nt;     // weights stream past the caches
+    int splits;  // parts of the reduction
+};
+
+template <int MODE, bool I8>
+TilePlan plan_tiles(const GemmArgs& g) {
+    const int eb = I8 ? 1 : 2;
+    const int64_t mean_rows = g.P / g.E;
+    TilePlan p{128, false, 1};
+    if (mean_rows <= 24)
+        p.rows = 32;
+    else if (mean_rows > 32 && tile_grid<MODE, 256, 256>(g) >= 512)
+        p.rows = 256;
+    p.nt = p.rows < 256 && mean_rows <= 32 && g.K * eb % 128 == 0 &&
+           static_cast<int64_t>(g.E) * g.N * g.K * eb > kStreamBytes;
+    const int64_t tiles = p.rows == 32 ? tile_grid<MODE, 128, 32>(g) : tile_grid<MODE, 128, 128>(g);
+    const int64_t stages = ((MODE == kProduct ? g.K : g.N) + 128 / eb - 1) / (128 / eb);
+    if (p.rows < 256 && tiles <= 128 && stages >= 16) {
+        const int64_t want = 512 / tiles, most = stages / 8;
+        p.splits = static_cast<int>(want < most ? want : most);
+        if (p.splits > 16) p.splits = 16;
+    }
+    return p;
+}
+
+// The sums of a split reduction: [splits][P][cols] 32-bit values, added in
+// order, then the output's scales and rounding.  A thread adds 4 columns.
+template <int MODE, bool I8>
+__global__ __launch_bounds__(kThreads) void join_splits_kernel(GemmArgs g, int splits) {
+    const int cols = MODE == kProduct ? g.N : g.K;
+    const int c = (blockIdx.x * kThreads + threadIdx.x) * 4;
+    const int64_t q = blockIdx.y + static_cast<int64_t>(blockIdx.z) * gridDim.y;
+    if (c >= cols || q >= g.P) return;
+    int e = 0;
+    if (g.offsets) {
+        if (q < g.offsets[0] || q >= g.offsets[g.E]) return;  // of no expert
+        if constexpr (I8) {
+            int hi = g.E - 1;  // last expert that begins at or before q
+            while (e < hi) {
+                const int mid = (e + hi + 1) >> 1;
+                if (g.offsets[mid] <= q) e = mid; else hi = mid - 1;
+            }
+        }
+    }
+    const int64_t at = q * cols + c, step = g.P * cols;
+    f32x4 v;
+    if constexpr (I8) {
+        i32x4 sum = {0, 0, 0, 0};
+        for (int s = 0; s < splits; ++s) sum += *reinterpret_cast<const i32x4*>(static_cast<const int32_t*>(g.ws) + s * step + at);
+        int64_t r = q;
+        if (g.pairs) {
+            r = g.pairs[q] / g.k;
+            r = r < 0 ? 0 : (r >= g.S ? g.S - 1 : r);
+        }
+        const float a = g.a_scale[r];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = static_cast<float>(sum[i]) * (a * g.w_scale[static_cast<int64_t>(e) * g.N + c + i]);
+    } else {
+        v = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4*>(static_cast<const float*>(g.ws) + s * step + at);
+    }
+    if (g.out_bf16) {
+        u32x2 h;
+        h[0] = pack_bf16(v[0], v[1]);
+        h[1] = pack_bf16(v[2], v[3]);
+        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(g.out) + at) = h;
+    } else {
+        f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + at);
+        if (g.accumulate) v += *o;
+        *o = v;
+    }
+}
+
+template <int MODE, bool I8>
+hipError_t launch(const GemmArgs& g, hipStream_t s) {
+    if (!gather_fits(g, I8 ? 1 : 2)) return launch_plain<MODE, I8>(g, s);
+    const TilePlan p = plan_tiles<MODE, I8>(g);
+    if (p.rows == 256) return launch_tiles<MODE, I8, 256, 256>(g, s);
+    hipError_t err;
+    if (p.rows == 32)
+        err = p.nt ? launch_tiles<MODE, I8, 128, 32, true>(g, s, p.splits)
+                   : launch_tiles<MODE, I8, 128, 32>(g, s, p.splits);
+    else
+        err = p.nt ? launch_tiles<MODE, I8, 128, 128, true>(g, s, p.splits)
+                   : launch_tiles<MODE, I8, 128, 128>(g, s, p.splits);
+    if (err != hipSuccess || p.splits == 1) return err;
+    const int cols = MODE == kProduct ? g.N : g.K;
+    const unsigned y = static_cast<unsigned>(g.P < 32768 ? g.P : 32768);
+    join_splits_kernel<MODE, I8><<<dim3((cols / 4 + kThreads - 1) / kThreads, y, static_cast<unsigned>((g.P + y - 1) / y)),
+                                   dim3(kThreads), 0, s>>>(g, p.splits);
+    return hipGetLastError();
+}
+
+// How the weight gradient of a shape runs.
+struct WgradPlan {
+    bool big;    // 256 x 256 tiles, else 128 x 128
+    int splits;  // parts of each expert's positions
+};
+
+WgradPlan plan_wgrad(const GemmArgs& g) {
+    // 256 x 256 tiles from about two for each compute unit on (256 experts of
+    // 2560 x 5120, 256 rows each: 2.6 against 3.5 ms; 24 experts of 776 x
+    // 1000 make 384 of them: 43 us on 1344 smaller ones)
+    WgradPlan p{static_cast<int64_t>((g.K + 255) / 256) * ((g.N + 255) / 256) * g.E >= 512, 1};
+    const int64_t tiles = static_cast<int64_t>((g.K + 127) / 128) * ((g.N + 127) / 128) * g.E;
+    if (!p.big && tiles <= 256 && g.P / g.E >= 512) {
+        int64_t n = 512 / tiles;
+        if (n > g.P / g.E / 256) n = g.P / g.E / 256;
+        if (n > kMaxE / g.E) n = kMaxE / g.E;  // the kernel's list of parts
+        if (n > 1) p.splits = static_cast<int>(n);
+    }
+    return p;
+}
+
+// dw (+)= the sums of the parts, in order; a thread adds 4 values.
+__global__ __launch_bounds__(kThreads) void join_wgrad_kernel(GemmArgs g, int64_t values, int splits) {
+    const int64_t i = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * 4;
+    if (i >= values) return;
+    const float* part = static_cast<const float*>(g.ws) + i;
+    f32x4 v = *reinterpret_cast<const f32x4*>(part);
+    for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const f32x4*>(part + s * values);
+    if (g.out_bf16) {
+        u32x2 h;
+        h[0] = pack_bf16(v[0], v[1]);
+        h[1] = pack_bf16(v[2], v[3]);
+        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(g.out) + i) = h;
+    } else {
+        f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + i);
+        if (g.accumulate) v += *o;
+        *o = v;
+    }
+}
+
 template <int BX, int BY, bool GATHER>
-hipError_t launch_wgrad(const GemmArgs& g, hipStream_t s) {
-    const int64_t tiles = static_cast<int64_t>((g.K + BX - 1) / BX) * ((g.N + BY - 1) / BY) * g.E;
+hipError_t launch_wgrad_tiles(const GemmArgs& g, hipStream_t s) {
+    const int64_t tiles = static_cast<int64_t>((g.K + BX - 1) / BX) * ((g.N + BY - 1) / BY) * g.E * g.splits;
     const int64_t most = static_cast<int64_t>(kNumCu) * WgradShape<BX, BY, GATHER>::kPerCu;
     const int64_t grid = tiles < most ? (tiles + kNumXcd - 1) / kNumXcd * kNumXcd : most;
     const dim3 blocks(static_cast<unsigned>(grid)), threads(kThreads);
@@ -198,27 +340,6 @@ hipError_t launch_wgrad(const GemmArgs& g, hipStream_t s) {
     else
         gemm_wgrad_kernel<BX, BY, GATHER, false, false><<<blocks, threads, 0, s>>>(g);
     return hipGetLastError();
-}
-
-template <int MODE, bool I8>
-hipError_t launch(const GemmArgs& g, hipStream_t s) {
-    // gathered rows are addressed with 32-bit offsets from a
-    if (g.pairs && g.S * static_cast<int64_t>(g.K) * (I8 ? 1 : 2) > static_cast<int64_t>(kNoRowOffset))
-        return launch_plain<MODE, I8>(g, s);
-    // 256 x 256 tiles move half the operand bytes of 128 x 128 ones (8192
-    // tokens over 256 experts: product 1.95 against 2.36 ms), but need about
-    // two tiles for each compute unit (5003 rows, 24 experts, 1000 x 776: 30
-    // against 21 us), and with few rows the smaller tile streams the weights
-    // faster (128 tokens over 256 experts: 1.08 against 1.10 ms).
-    const int64_t mean_rows = g.P / g.E;
-    if constexpr (MODE == kWeightGrad) {
-        const bool big = tile_grid<MODE, 256, 256>(g) >= 512;
-        if (g.pairs) return big ? launch_wgrad<256, 256, true>(g, s) : launch_wgrad<128, 128, true>(g, s);
-        return big ? launch_wgrad<256, 256, false>(g, s) : launch_wgrad<128, 128, false>(g, s);
-    }
-    if (tile_grid<MODE, 256, 256>(g) >= 512 && (MODE == kWeightGrad || mean_rows > 32))
-        return launch_tiles<MODE, I8, 256, 256>(g, s);
-    return launch_tiles<MODE, I8, 128, 128>(g, s);
 }
 
 // One row of bf16 per workgroup: its largest magnitude, then its codes.
@@ -270,13 +391,43 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const uint16_t*
 
 }  // namespace
 
-size_t grouped_ws_bytes(const GemmArgs&) { return 0; }
+size_t grouped_ws_bytes(const GemmArgs& g) {
+    if (g.P == 0) return 0;
+    size_t most = 0;
+    auto need = [&](int splits, int64_t values) {
+        const size_t n = splits > 1 ? static_cast<size_t>(splits) * static_cast<size_t>(values) * 4 : 0;
+        most = n > most ? n : most;
+    };
+    need(plan_tiles<kProduct, false>(g).splits, g.P * g.N);
+    need(plan_tiles<kProduct, true>(g).splits, g.P * g.N);
+    need(plan_tiles<kInputGrad, false>(g).splits, g.P * g.K);
+    need(plan_wgrad(g).splits, static_cast<int64_t>(g.E) * g.N * g.K);
+    return most;
+}
 
 hipError_t launch_grouped_gemm(const GemmArgs& g, hipStream_t s) { return launch<kProduct, false>(g, s); }
 
 hipError_t launch_grouped_dgrad(const GemmArgs& g, hipStream_t s) { return launch<kInputGrad, false>(g, s); }
 
-hipError_t launch_grouped_wgrad(const GemmArgs& g, hipStream_t s) { return launch<kWeightGrad, false>(g, s); }
+hipError_t launch_grouped_wgrad(const GemmArgs& g, hipStream_t s) {
+    if (!gather_fits(g, 2)) return launch_plain<kWeightGrad, false>(g, s);
+    const WgradPlan p = plan_wgrad(g);
+    if (p.big) return g.pairs ? launch_wgrad_tiles<256, 256, true>(g, s) : launch_wgrad_tiles<256, 256, false>(g, s);
+    if (p.splits == 1)
+        return g.pairs ? launch_wgrad_tiles<128, 128, true>(g, s) : launch_wgrad_tiles<128, 128, false>(g, s);
+    GemmArgs part = g;
+    part.out = g.ws;
+    part.out_bf16 = false;
+    part.accumulate = false;
+    part.splits = p.splits;
+    const hipError_t err =
+        g.pairs ? launch_wgrad_tiles<128, 128, true>(part, s) : launch_wgrad_tiles<128, 128, false>(part, s);
+    if (err != hipSuccess) return err;
+    const int64_t values = static_cast<int64_t>(g.E) * g.N * g.K;
+    const int64_t blocks = (values / 4 + kThreads - 1) / kThreads;
+    join_wgrad_kernel<<<dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s>>>(g, values, p.splits);
+    return hipGetLastError();
+}
 
 hipError_t launch_grouped_int8(const GemmArgs& g, hipStream_t s) { return launch<kProduct, true>(g, s); }
 

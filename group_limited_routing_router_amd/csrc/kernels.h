@@ -30,7 +30,8 @@ struct GemmArgs {
     void* out;
     bool out_bf16;           // out is bf16, else fp32
     bool accumulate;         // out += (fp32)
-    void* ws;
+    void* ws;                // sums of a split reduction
+    int splits;              // weight gradient: parts of each expert's positions
 };
 
 // Pairs handled by one block of the counting sort.

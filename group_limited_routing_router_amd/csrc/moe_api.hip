@@ -529,6 +529,7 @@ moe::GemmArgs gemm_args(const moe_gemm_problem& g) {
     while ((1LL << b) < g.k) ++b;
     a.k_magic = static_cast<uint32_t>((1ULL << (31 + b)) / static_cast<uint64_t>(g.k) + 1);
     a.k_shift = b - 1;
+    a.splits = 1;
     return a;
 }
 

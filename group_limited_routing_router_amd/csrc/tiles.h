@@ -84,10 +84,12 @@ __device__ bool find_tile(const int32_t* offsets, int64_t P, int E, int ncol_til
         if (lane >= d) incl += v;
     }
     int32_t* s_wave_total = s_tstart + (kMaxE + 1);
-    if (lane == kWave - 1) s_wave_total[wave] = incl;
+    if (lane == kWave - 1 && wave < kWaves) s_wave_total[wave] = incl;
     __syncthreads();
-    for (int w = 0; w < wave; ++w) incl += s_wave_total[w];
-    s_tstart[tid + 1] = incl;  // exclusive prefix over positions; s_tstart[E] = total row tiles
+    if (tid < kMaxE) {  // larger workgroups: the waves past the experts only wait
+        for (int w = 0; w < wave; ++w) incl += s_wave_total[w];
+        s_tstart[tid + 1] = incl;  // exclusive prefix over positions; s_tstart[E] = total row tiles
+    }
     if (tid == 0) s_tstart[0] = 0;
     __syncthreads();
     const int64_t total = static_cast<int64_t>(s_tstart[E]) * ncol_tiles;
@@ -138,9 +140,21 @@ __device__ bool find_tile(const int32_t* offsets, int64_t P, int E, int ncol_til
 // (contiguous, lane order); voffset is the lane's byte offset, soffset a
 // uniform one.  The compiler does not see the load: the caller waits for it
 // with wait_vmcnt.
+// NT streams past the caches.
+template <bool NT = false>
 __device__ __forceinline__ void dma_load16(uint32_t lds_byte_addr, __amdgpu_buffer_rsrc_t rsrc,
                                            uint32_t voffset, uint32_t soffset) {
-    asm volatile(
+    if constexpr (NT)
+        asm volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %1, %2, %3 offen nt lds"
+        :
+        : "s"(__builtin_amdgcn_readfirstlane(lds_byte_addr)), "v"(voffset), "s"(rsrc),
+          "s"(__builtin_amdgcn_readfirstlane(soffset))
+        : "memory", "m0");
+    else
+        asm volatile(
         "s_mov_b32 m0, %0\n\t"
         "s_nop 0\n\t"
         "buffer_load_dwordx4 %1, %2, %3 offen lds"

@@ -85,6 +85,12 @@ SHAPES = [
     (600, 5, 304, 784, 3, "random"),
     (1031, 9, 1008, 272, 1, "random"),
     (2100, 4, 256, 640, 6, "random"),
+    (5, 1, 128, 4112, 1, "even"),       # split reductions: the product's
+    (40, 2, 192, 2064, 2, "random"),
+    (3, 1, 2064, 128, 1, "even"),       # ... the input gradient's
+    (70, 2, 3088, 144, 1, "random"),
+    (2500, 2, 144, 176, 1, "random"),   # ... the weight gradient's
+    (1700, 1, 64, 80, 2, "even"),
 ]
 IDS = ["P%d_E%d_N%d_K%d_k%d_%s" % s for s in SHAPES]
 
@@ -110,7 +116,8 @@ def test_multiples_of_eight(moe, shape, op):
 
 
 @pytest.mark.parametrize("op", ["product", "input_grad", "weight_grad", "int8"])
-@pytest.mark.parametrize("shape", [(90, 4, 64, 96, 1), (500, 3, 272, 320, 2), (40, 1, 512, 512, 1)],
+@pytest.mark.parametrize("shape", [(90, 4, 64, 96, 1), (500, 3, 272, 320, 2), (40, 1, 512, 512, 1),
+                                   (40, 2, 96, 2064, 1), (40, 2, 2064, 96, 2), (1500, 1, 80, 96, 2)],
                          ids=lambda s: "P%d_E%d_N%d_K%d_k%d" % s)
 def test_rows_of_no_expert(moe, shape, op):
     """Positions before the first expert's and behind the last's: not read
@@ -135,7 +142,8 @@ def test_one_group_without_offsets(moe, op, P, N, K):
 
 
 @pytest.mark.parametrize("op", ["input_grad", "weight_grad"])
-@pytest.mark.parametrize("shape", [(60, 4, 72, 40, 1), (700, 3, 272, 320, 2), (9, 1, 640, 768, 1)],
+@pytest.mark.parametrize("shape", [(60, 4, 72, 40, 1), (700, 3, 272, 320, 2), (9, 1, 640, 768, 1),
+                                   (6, 1, 2056, 72, 1), (1500, 1, 72, 80, 2)],
                          ids=lambda s: "P%d_E%d_N%d_K%d_k%d" % s)
 def test_accumulate(moe, op, shape):
     print(f"[case] {op} {shape}", flush=True)
