@@ -197,23 +197,60 @@ struct TilePlan {
     int splits;  // parts of the reduction
 };
 
+// Microseconds of `tiles` workgroups over `stages` stages each: a round holds
+// one 256-row tile on each compute unit or two of the smaller ones, and costs
+// about 4 us beside its stages (measured: a stage of 128 bytes takes 1.85 us on
+// 256 rows; 0.6 us on 128 and 0.22 us on 32 with a compute unit to itself, 1.1
+// and 0.45 us with two on it).
+float tile_time(int rows, float tiles, float stages) {
+    if (rows == 256) return (tiles > kNumCu ? tiles / kNumCu : 1.0f) * (1.85f * stages + 4.0f);
+    const float alone = rows == 128 ? 0.6f : 0.22f, paired = rows == 128 ? 1.1f : 0.45f;
+    if (tiles <= kNumCu) return alone * stages + 4.0f;
+    return (tiles > 2 * kNumCu ? tiles / (2 * kNumCu) : 1.0f) * (paired * stages + 4.0f);
+}
+
+// The host does not read the experts' counts: a mean expert is taken, with
+// half a tile more for the ragged end.
 template <int MODE, bool I8>
 TilePlan plan_tiles(const GemmArgs& g) {
     const int eb = I8 ? 1 : 2;
-    const int64_t mean_rows = g.P / g.E;
-    TilePlan p{128, false, 1};
-    if (mean_rows <= 24)
-        p.rows = 32;
-    else if (mean_rows > 32 && tile_grid<MODE, 256, 256>(g) >= 512)
-        p.rows = 256;
-    p.nt = p.rows < 256 && mean_rows <= 32 && g.K * eb % 128 == 0 &&
-           static_cast<int64_t>(g.E) * g.N * g.K * eb > kStreamBytes;
-    const int64_t tiles = p.rows == 32 ? tile_grid<MODE, 128, 32>(g) : tile_grid<MODE, 128, 128>(g);
-    const int64_t stages = ((MODE == kProduct ? g.K : g.N) + 128 / eb - 1) / (128 / eb);
-    if (p.rows < 256 && tiles <= 128 && stages >= 16) {
-        const int64_t want = 512 / tiles, most = stages / 8;
-        p.splits = static_cast<int>(want < most ? want : most);
-        if (p.splits > 16) p.splits = 16;
+    const int cols = MODE == kProduct ? g.N : g.K;
+    const float mean_rows = static_cast<float>(g.P) / g.E;
+    const bool large = static_cast<int64_t>(g.E) * g.N * g.K * eb > kStreamBytes;
+    const float stages = static_cast<float>(((MODE == kProduct ? g.K : g.N) + 128 / eb - 1) / (128 / eb));
+    auto tiles_of = [&](int rows) {
+        const float experts = static_cast<float>(g.E < g.P ? g.E : g.P);
+        const float each = g.E == 1 ? static_cast<float>((g.P + rows - 1) / rows) : mean_rows / rows + 0.45f;
+        const int width = rows == 256 ? 256 : 128;
+        return experts * (each > 1.0f ? each : 1.0f) * static_cast<float>((cols + width - 1) / width);
+    };
+    TilePlan p{256, false, 1};
+    if (large && mean_rows > 32) return p;  // the fewest reads of the weights (4096 tokens, busy
+                                            // and idle experts: 1.46 against 1.68 ms on 128 rows)
+    if (large) {
+        // the weight stream is the time: the tile that takes an expert's rows
+        // at once and keeps the most loads in flight (256 experts of 2560 x
+        // 5120: 4 rows each 0.97 ms on 32, 1.07 on 128 rows; 24 rows each 1.10
+        // and 1.09 ms)
+        p.rows = mean_rows <= 24 ? 32 : 128;
+        // past the caches where rows are whole lines (0.97 against 1.07 ms;
+        // rows of 1776 bytes: 452 against 381 us)
+        p.nt = g.K * eb % 128 == 0;
+    }
+    float best = -1.0f;
+    for (int rows : {32, 128, 256}) {
+        if (large && rows != p.rows) continue;
+        for (int splits = 1; splits <= (rows == 256 ? 1 : 16); splits *= 2) {
+            if (splits > 1 && (stages < 4 * splits || large)) break;
+            float t = tile_time(rows, tiles_of(rows) * splits, stages / splits);
+            // the sums written and read, and one more launch
+            if (splits > 1) t += 4.0f + 2.0f * splits * static_cast<float>(g.P) * cols * 4.0f / 5e6f;
+            if (best < 0.0f || t < best) {
+                best = t;
+                p.rows = rows;
+                p.splits = splits;
+            }
+        }
     }
     return p;
 }
@@ -342,50 +379,87 @@ hipError_t launch_wgrad_tiles(const GemmArgs& g, hipStream_t s) {
     return hipGetLastError();
 }
 
-// One row of bf16 per workgroup: its largest magnitude, then its codes.
-__global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const uint16_t* x, int K, int8_t* codes,
-                                                                 float* scales) {
+// The code of x in a row whose largest magnitude is m, 1 / m rounded to fp32:
+// 127 x / m to the nearest, ties to even, exactly.  127 x is exact (15 bits),
+// the product with 1 / m within one of the code, and the remainder 127 x - r m
+// exact, so it tells on which side of the half way point the quotient lies (x
+// = m / 2 lies on one).
+__device__ __forceinline__ int code_of(float x, float m, float inv) {
+    const float y = 127.0f * x;
+    float r = rintf(y * inv);
+    const float e = fmaf(-r, m, y), e2 = 2.0f * fabsf(e);
+    const bool odd = static_cast<int>(r) & 1;
+    if (e2 > m || (e2 == m && odd)) r += copysignf(1.0f, e);
+    return static_cast<int>(r);
+}
+
+// Rows of bf16 as 8-bit codes with one scale each, LANES lanes a row.  A row
+// is read once and stays in registers (CHUNKS 16-byte pieces a lane); CHUNKS =
+// 0 reads it twice (K > 8192).  Bound by memory: 8192 rows of 5120 (126 MB
+// read and written).
+template <int LANES, int CHUNKS>
+__global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const uint16_t* x, int64_t rows, int K,
+                                                                 int8_t* codes, float* scales) {
     __shared__ float s_max[kWaves];
-    __shared__ int s_bad[kWaves];
-    const int64_t r = blockIdx.x;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid % LANES;
+    const int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads / LANES) + tid / LANES;
+    if (LANES == kWave && r >= rows) return;  // whole waves; with one row a workgroup there are no others
     const uint16_t* row = x + r * K;
-    float m = 0.0f;
-    int bad = 0;
-    for (int c = tid * 8; c < K; c += kThreads * 8) {
-        const u32x4 v = ld16(row + c);
-        const uint16_t* h = reinterpret_cast<const uint16_t*>(&v);
-        for (int i = 0; i < 8; ++i) {
-            m = fmaxf(m, fabsf(bf16_to_f32(h[i])));
-            bad |= (h[i] & 0x7f80) == 0x7f80;
+    // magnitudes as integers: in this order infinity and NaN come last
+    uint32_t top = 0;
+    u32x4 v[CHUNKS > 0 ? CHUNKS : 1];
+    auto look = [&](const u32x4& p) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            top = max(top, p[i] & 0x7fffu);
+            top = max(top, p[i] >> 16 & 0x7fffu);
         }
+    };
+    if constexpr (CHUNKS > 0) {
+#pragma unroll
+        for (int j = 0; j < CHUNKS; ++j) {
+            const int c = (j * LANES + lane) * 8;
+            v[j] = c < K ? ld16(row + c) : u32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int j = 0; j < CHUNKS; ++j) look(v[j]);
+    } else {
+        for (int c = lane * 8; c < K; c += LANES * 8) look(ld16(row + c));
     }
-    for (int d = 32; d; d >>= 1) {
-        m = fmaxf(m, __shfl_xor(m, d, kWave));
-        bad |= __shfl_xor(bad, d, kWave);
+#pragma unroll
+    for (int d = 32; d; d >>= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d, kWave)));
+    float m = bf16_to_f32(static_cast<uint16_t>(top));
+    if constexpr (LANES > kWave) {
+        if ((tid & 63) == 0) s_max[tid >> 6] = __uint_as_float(top);  // the bits
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) top = max(top, __float_as_uint(s_max[w]));
+        m = bf16_to_f32(static_cast<uint16_t>(top));
     }
-    if ((tid & 63) == 0) {
-        s_max[tid >> 6] = m;
-        s_bad[tid >> 6] = bad;
-    }
-    __syncthreads();
-    for (int w = 0; w < kWaves; ++w) {
-        m = fmaxf(m, s_max[w]);
-        bad |= s_bad[w];
-    }
+    const bool bad = top >= 0x7f80u;
     const bool zero = bad || m < 0x1p-100f;
-    // 127 x is exact in fp32 (15 bits) and the division correctly rounded, so
-    // a quotient half way between two codes is met exactly (x = amax / 2 is
-    // one); large rows are scaled down first, since 127 x would overflow
+    if (lane == 0) scales[r] = bad ? __builtin_nanf("") : (zero ? 1.0f : m / 127.0f);
+    // large rows are scaled down first, since 127 x would overflow
     const float shrink = m > 0x1p100f ? 0x1p-30f : 1.0f;
-    if (tid == 0) scales[r] = bad ? __builtin_nanf("") : (zero ? 1.0f : m / 127.0f);
-    for (int c = tid * 8; c < K; c += kThreads * 8) {
-        const u32x4 v = ld16(row + c);
-        const uint16_t* h = reinterpret_cast<const uint16_t*>(&v);
-        union { int8_t b[8]; uint64_t u; } o;
-        for (int i = 0; i < 8; ++i)
-            o.b[i] = zero ? 0 : static_cast<int8_t>(rintf(bf16_to_f32(h[i]) * shrink * 127.0f / (m * shrink)));
-        *reinterpret_cast<uint64_t*>(codes + r * K + c) = o.u;
+    const float ms = m * shrink, inv = 1.0f / ms;
+    auto write = [&](int c, const u32x4& p) {
+        uint64_t o = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float xi = __uint_as_float(i & 1 ? p[i / 2] & 0xffff0000u : p[i / 2] << 16);
+            const int code = zero ? 0 : code_of(xi * shrink, ms, inv);
+            o |= static_cast<uint64_t>(static_cast<uint8_t>(code)) << (8 * i);
+        }
+        *reinterpret_cast<uint64_t*>(codes + r * K + c) = o;
+    };
+    if constexpr (CHUNKS > 0) {
+#pragma unroll
+        for (int j = 0; j < CHUNKS; ++j) {
+            const int c = (j * LANES + lane) * 8;
+            if (c < K) write(c, v[j]);
+        }
+    } else {
+        for (int c = lane * 8; c < K; c += LANES * 8) write(c, ld16(row + c));
     }
 }
 
@@ -434,7 +508,15 @@ hipError_t launch_grouped_int8(const GemmArgs& g, hipStream_t s) { return launch
 hipError_t launch_quantize_rows(int64_t rows, int K, const uint16_t* x, int8_t* codes, float* scales,
                                 hipStream_t s) {
     if (rows <= 0) return hipSuccess;
-    quantize_rows_kernel<<<dim3(static_cast<unsigned>(rows)), dim3(kThreads), 0, s>>>(x, K, codes, scales);
+    const dim3 threads(kThreads), whole(static_cast<unsigned>(rows)), waves(static_cast<unsigned>((rows + 3) / 4));
+    if (K <= 512)
+        quantize_rows_kernel<kWave, 1><<<waves, threads, 0, s>>>(x, rows, K, codes, scales);
+    else if (K <= 2048)
+        quantize_rows_kernel<kWave, 4><<<waves, threads, 0, s>>>(x, rows, K, codes, scales);
+    else if (K <= 8192)
+        quantize_rows_kernel<kThreads, 4><<<whole, threads, 0, s>>>(x, rows, K, codes, scales);
+    else
+        quantize_rows_kernel<kThreads, 0><<<whole, threads, 0, s>>>(x, rows, K, codes, scales);
     return hipGetLastError();
 }
 

@@ -289,17 +289,21 @@ def moe_forward_noalloc(p, x, w_router, bias, w_gate, w_up, w_down, out, topk_id
 #
 # These also check what the C side cannot see: that each tensor has the type
 # and at least the elements the call takes, is contiguous and lies on the
-# current device.
+# current device.  The calls are as short as the kernels they launch, so the
+# device is asked for once and the library's functions are looked up once.
 
-def _arg(t, name, dtype, n, nullable=False):
+_BF16, _F32, _I32, _I8 = torch.bfloat16, torch.float32, torch.int32, torch.int8
+
+
+def _arg(t, name, dtype, n, device, nullable=False):
     """The device address of tensor t after those checks."""
     if t is None:
         if nullable:
             return None
         raise ValueError(f"{name} is None")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} dtype {t.dtype} is not {dtype}")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, not on the current GPU")
     if not t.is_contiguous():
         raise ValueError(f"{name} is not contiguous")
@@ -308,82 +312,94 @@ def _arg(t, name, dtype, n, nullable=False):
     return t.data_ptr()
 
 
-def _ws(ws):
+def _ws_args(ws, device):
     if ws is None:
         return None, 0
-    nbytes = ws.numel() * ws.element_size()
-    return _arg(ws, "ws", ws.dtype, 0), nbytes
+    return _arg(ws, "ws", ws.dtype, 0, device), ws.numel() * ws.element_size()
+
+
+def _on(stream, device):
+    """The handle of `stream` (the current one of the device if None)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def moe_gemm_workspace_bytes(g: MoEGemmProblem) -> int:
-    return int(load_library().moe_gemm_workspace_bytes(ctypes.byref(g)))
+    return int(load_library().moe_gemm_workspace_bytes(g))
 
 
 def moe_grouped_gemm(g, a, sorted_pairs, expert_offsets, w, out, ws=None, stream=None):
     """out [P,N] (fp32 or bf16) = a[row(q)] . w[e]^T for each position q."""
-    code = _dtype_code(out)
-    wp, wn = _ws(ws)
-    _check(load_library().moe_grouped_gemm(
-        ctypes.byref(g), _arg(a, "a", torch.bfloat16, g.S * g.K),
-        _arg(sorted_pairs, "sorted_pairs", torch.int32, g.P, True),
-        _arg(expert_offsets, "expert_offsets", torch.int32, g.E + 1, g.E == 1),
-        _arg(w, "w", torch.bfloat16, g.E * g.N * g.K), _arg(out, "out", out.dtype, g.P * g.N),
-        code, wp, wn, _stream(stream)))
+    lib = _lib or load_library()
+    dev = torch.cuda.current_device()
+    P, E, N, K = g.P, g.E, g.N, g.K
+    wp, wn = _ws_args(ws, dev)
+    _check(lib.moe_grouped_gemm(
+        g, _arg(a, "a", _BF16, g.S * K, dev), _arg(sorted_pairs, "sorted_pairs", _I32, P, dev, True),
+        _arg(expert_offsets, "expert_offsets", _I32, E + 1, dev, E == 1),
+        _arg(w, "w", _BF16, E * N * K, dev), _arg(out, "out", out.dtype, P * N, dev),
+        _dtype_code(out), wp, wn, _on(stream, dev)))
 
 
 def moe_grouped_gemm_dgrad(g, dout, expert_offsets, w, da, ws=None, accumulate=False,
                            stream=None):
     """da [P,K] (fp32 or bf16) = dout[q] . w[e]; da += with accumulate."""
-    code = _dtype_code(da)
-    wp, wn = _ws(ws)
-    _check(load_library().moe_grouped_gemm_dgrad(
-        ctypes.byref(g), _arg(dout, "dout", torch.bfloat16, g.P * g.N),
-        _arg(expert_offsets, "expert_offsets", torch.int32, g.E + 1, g.E == 1),
-        _arg(w, "w", torch.bfloat16, g.E * g.N * g.K), _arg(da, "da", da.dtype, g.P * g.K),
-        code, int(bool(accumulate)), wp, wn, _stream(stream)))
+    lib = _lib or load_library()
+    dev = torch.cuda.current_device()
+    P, E, N, K = g.P, g.E, g.N, g.K
+    wp, wn = _ws_args(ws, dev)
+    _check(lib.moe_grouped_gemm_dgrad(
+        g, _arg(dout, "dout", _BF16, P * N, dev),
+        _arg(expert_offsets, "expert_offsets", _I32, E + 1, dev, E == 1),
+        _arg(w, "w", _BF16, E * N * K, dev), _arg(da, "da", da.dtype, P * K, dev),
+        _dtype_code(da), 1 if accumulate else 0, wp, wn, _on(stream, dev)))
 
 
 def moe_grouped_gemm_wgrad(g, dout, a, sorted_pairs, expert_offsets, dw, ws=None,
                            accumulate=False, stream=None):
     """dw [E,N,K] (fp32 or bf16) = sum over each expert's positions of
     dout[q]^T a[row(q)]; dw += with accumulate."""
-    code = _dtype_code(dw)
-    wp, wn = _ws(ws)
-    empty = g.P == 0
-    _check(load_library().moe_grouped_gemm_wgrad(
-        ctypes.byref(g), _arg(dout, "dout", torch.bfloat16, g.P * g.N, empty),
-        _arg(a, "a", torch.bfloat16, 0 if empty else g.S * g.K, empty),
-        _arg(sorted_pairs, "sorted_pairs", torch.int32, g.P, True),
-        _arg(expert_offsets, "expert_offsets", torch.int32, g.E + 1, g.E == 1),
-        _arg(dw, "dw", dw.dtype, g.E * g.N * g.K), code, int(bool(accumulate)), wp, wn,
-        _stream(stream)))
+    lib = _lib or load_library()
+    dev = torch.cuda.current_device()
+    P, E, N, K = g.P, g.E, g.N, g.K
+    wp, wn = _ws_args(ws, dev)
+    _check(lib.moe_grouped_gemm_wgrad(
+        g, _arg(dout, "dout", _BF16, P * N, dev, P == 0),
+        _arg(a, "a", _BF16, g.S * K if P else 0, dev, P == 0),
+        _arg(sorted_pairs, "sorted_pairs", _I32, P, dev, True),
+        _arg(expert_offsets, "expert_offsets", _I32, E + 1, dev, E == 1),
+        _arg(dw, "dw", dw.dtype, E * N * K, dev), _dtype_code(dw), 1 if accumulate else 0, wp, wn,
+        _on(stream, dev)))
 
 
 def moe_quantize_rows_int8(x, codes, scales, stream=None):
     """The rows of x [rows,K] bf16 as int8 codes [rows,K] and fp32 scales
     [rows] (amax / 127)."""
+    lib = _lib or load_library()
+    dev = torch.cuda.current_device()
     if x.dim() != 2:
         raise ValueError(f"x has {x.dim()} dimensions, needs 2")
     rows, K = x.shape
-    _check(load_library().moe_quantize_rows_int8(
-        rows, K, _arg(x, "x", torch.bfloat16, 0), _arg(codes, "codes", torch.int8, rows * K),
-        _arg(scales, "scales", torch.float32, rows), _stream(stream)))
+    _check(lib.moe_quantize_rows_int8(
+        rows, K, _arg(x, "x", _BF16, 0, dev), _arg(codes, "codes", _I8, rows * K, dev),
+        _arg(scales, "scales", _F32, rows, dev), _on(stream, dev)))
 
 
 def moe_grouped_gemm_int8(g, a, a_scale, sorted_pairs, expert_offsets, w, w_scale, out, ws=None,
                           stream=None):
     """out [P,N] (fp32 or bf16) = a_scale[row(q)] w_scale[e] (a[row(q)] .
     w[e]^T) on int8 codes."""
-    code = _dtype_code(out)
-    wp, wn = _ws(ws)
-    _check(load_library().moe_grouped_gemm_int8(
-        ctypes.byref(g), _arg(a, "a", torch.int8, g.S * g.K),
-        _arg(a_scale, "a_scale", torch.float32, g.S),
-        _arg(sorted_pairs, "sorted_pairs", torch.int32, g.P, True),
-        _arg(expert_offsets, "expert_offsets", torch.int32, g.E + 1, g.E == 1),
-        _arg(w, "w", torch.int8, g.E * g.N * g.K),
-        _arg(w_scale, "w_scale", torch.float32, g.E * g.N), _arg(out, "out", out.dtype, g.P * g.N),
-        code, wp, wn, _stream(stream)))
+    lib = _lib or load_library()
+    dev = torch.cuda.current_device()
+    P, S, E, N, K = g.P, g.S, g.E, g.N, g.K
+    wp, wn = _ws_args(ws, dev)
+    _check(lib.moe_grouped_gemm_int8(
+        g, _arg(a, "a", _I8, S * K, dev), _arg(a_scale, "a_scale", _F32, S, dev),
+        _arg(sorted_pairs, "sorted_pairs", _I32, P, dev, True),
+        _arg(expert_offsets, "expert_offsets", _I32, E + 1, dev, E == 1),
+        _arg(w, "w", _I8, E * N * K, dev), _arg(w_scale, "w_scale", _F32, E * N, dev),
+        _arg(out, "out", out.dtype, P * N, dev), _dtype_code(out), wp, wn, _on(stream, dev)))
 
 
 def moe_peak_stream_read(buf, sink, workgroups, nontemporal=False, stream=None):
