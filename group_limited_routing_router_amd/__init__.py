@@ -12,7 +12,9 @@ _BINDING_NAMES = (
     "moe_forward_fp8", "moe_forward_noalloc", "moe_peak_stream_read", "moe_peak_mfma_bf16",
     "moe_peak_mfma_stream", "moe_gemm_workspace_bytes", "moe_grouped_gemm",
     "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad", "moe_quantize_rows_int8",
-    "moe_grouped_gemm_int8", "MoEGemmProblem",
+    "moe_grouped_gemm_int8", "moe_int8_workspace_bytes", "moe_expert_ffn_int8",
+    "moe_forward_int8", "moe_backward_workspace_bytes", "moe_expert_ffn_backward",
+    "MoEGemmProblem",
     "moe_workspace_bytes", "MoEProblem", "MoEError", "DTYPE_F32", "DTYPE_BF16",
     "load_library", "library_path",
 )

@@ -106,4 +106,13 @@ hipError_t launch_grouped_int8(const GemmArgs& g, hipStream_t s);
 hipError_t launch_quantize_rows(int64_t rows, int K, const uint16_t* x, int8_t* codes, float* scales,
                                 hipStream_t s);
 
+// h = silu(g) u of the rows that belong to an expert, as int8 codes [P,I] with
+// one scale per row [P].
+hipError_t launch_swiglu_quantize(const float* g, const float* u, int64_t P, int I, const int32_t* offsets, int E,
+                                  int8_t* codes, float* scales, hipStream_t s);
+
+// h = silu(g) u and the gradients of g and u from dh, all rounded to bf16.
+hipError_t launch_swiglu_backward(const float* g, const float* u, const float* dh, int64_t values, uint16_t* h,
+                                  uint16_t* dg, uint16_t* du, hipStream_t s);
+
 }  // namespace moe

@@ -537,8 +537,7 @@ size_t gemm_ws_bytes(const moe_gemm_problem& g) {
     return moe::grouped_ws_bytes(gemm_args(g));
 }
 
-moe_status check_gemm_ws(const moe_gemm_problem& g, const void* ws, size_t ws_bytes) {
-    const size_t need = gemm_ws_bytes(g);
+moe_status check_ws_bytes(size_t need, const void* ws, size_t ws_bytes) {
     if (need == 0) return MOE_OK;
     if (!ws) return fail(MOE_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", need);
     if (reinterpret_cast<uintptr_t>(ws) % 16 != 0)
@@ -546,6 +545,10 @@ moe_status check_gemm_ws(const moe_gemm_problem& g, const void* ws, size_t ws_by
     if (ws_bytes < need)
         return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, need %zu", ws_bytes, need);
     return MOE_OK;
+}
+
+moe_status check_gemm_ws(const moe_gemm_problem& g, const void* ws, size_t ws_bytes) {
+    return check_ws_bytes(gemm_ws_bytes(g), ws, ws_bytes);
 }
 
 }  // namespace
@@ -669,6 +672,270 @@ MOE_EXPORT moe_status moe_grouped_gemm_int8(const moe_gemm_problem* g, const int
     x.out_bf16 = out_dtype == MOE_DTYPE_BF16;
     x.ws = ws;
     return hip_status(moe::launch_grouped_int8(x, stream), "grouped int8 gemm launch");
+}
+
+// ---- the experts on these products ----
+
+namespace {
+
+moe_gemm_problem gate_shape(const moe_problem& p) {  // x -> g, u
+    return moe_gemm_problem{p.T * p.k, p.T, p.E, p.I, p.H, p.k};
+}
+
+moe_gemm_problem down_shape(const moe_problem& p) {  // h -> y
+    return moe_gemm_problem{p.T * p.k, p.T * p.k, p.E, p.H, p.I, 1};
+}
+
+// What follows the forward pass's own workspace: the products' sums, their
+// operands, the scratch of split reductions.
+struct Int8Layout {
+    size_t x, x_scale, g, u, h, h_scale, sums, total;
+};
+
+Int8Layout int8_layout(const moe_problem& p) {
+    const size_t P = static_cast<size_t>(p.T) * static_cast<size_t>(p.k), T = static_cast<size_t>(p.T);
+    const size_t H = static_cast<size_t>(p.H), I = static_cast<size_t>(p.I);
+    const size_t a = gemm_ws_bytes(gate_shape(p)), b = gemm_ws_bytes(down_shape(p));
+    Int8Layout L{};
+    size_t o = layout_of(p).total;
+    L.x = o;       o += align_up(T * H);
+    L.x_scale = o; o += align_up(T * 4);
+    L.g = o;       o += align_up(P * I * 4);
+    L.u = o;       o += align_up(P * I * 4);
+    L.h = o;       o += align_up(P * I);
+    L.h_scale = o; o += align_up(P * 4);
+    L.sums = o;    o += align_up(a > b ? a : b);
+    L.total = o;
+    return L;
+}
+
+struct BackwardLayout {
+    size_t g, u, dh, h, dg, du, sums, total;
+};
+
+BackwardLayout backward_layout(const moe_problem& p) {
+    const size_t PI = static_cast<size_t>(p.T) * static_cast<size_t>(p.k) * static_cast<size_t>(p.I);
+    const size_t a = gemm_ws_bytes(gate_shape(p)), b = gemm_ws_bytes(down_shape(p));
+    BackwardLayout L{};
+    size_t o = 0;
+    L.g = o;    o += align_up(PI * 4);
+    L.u = o;    o += align_up(PI * 4);
+    L.dh = o;   o += align_up(PI * 4);
+    L.h = o;    o += align_up(PI * 2);
+    L.dg = o;   o += align_up(PI * 2);
+    L.du = o;   o += align_up(PI * 2);
+    L.sums = o; o += align_up(a > b ? a : b);
+    L.total = o;
+    return L;
+}
+
+struct Int8Weights {
+    const int8_t *gate, *up, *down;
+    const float *s_gate, *s_up, *s_down;
+};
+
+hipError_t run_ffn_int8(const moe_problem& p, const moe_bf16* x, const int32_t* sorted, const int32_t* off,
+                        const Int8Weights& w, float* y, void* ws, hipStream_t stream) {
+    const Int8Layout L = int8_layout(p);
+    int8_t* xc = at<int8_t>(ws, L.x);
+    float* xs = at<float>(ws, L.x_scale);
+    hipError_t e = moe::launch_quantize_rows(p.T, p.H, x, xc, xs, stream);
+    if (e != hipSuccess) return e;
+    moe::GemmArgs a = gemm_args(gate_shape(p));
+    a.a = xc;
+    a.a_scale = xs;
+    a.pairs = sorted;
+    a.offsets = off;
+    a.ws = at<char>(ws, L.sums);
+    a.w = w.gate;
+    a.w_scale = w.s_gate;
+    a.out = at<float>(ws, L.g);
+    e = moe::launch_grouped_int8(a, stream);
+    if (e != hipSuccess) return e;
+    a.w = w.up;
+    a.w_scale = w.s_up;
+    a.out = at<float>(ws, L.u);
+    e = moe::launch_grouped_int8(a, stream);
+    if (e != hipSuccess) return e;
+    e = moe::launch_swiglu_quantize(at<float>(ws, L.g), at<float>(ws, L.u), a.P, p.I, off, p.E,
+                                    at<int8_t>(ws, L.h), at<float>(ws, L.h_scale), stream);
+    if (e != hipSuccess) return e;
+    moe::GemmArgs d = gemm_args(down_shape(p));
+    d.a = at<int8_t>(ws, L.h);
+    d.a_scale = at<float>(ws, L.h_scale);
+    d.offsets = off;
+    d.ws = at<char>(ws, L.sums);
+    d.w = w.down;
+    d.w_scale = w.s_down;
+    d.out = y;
+    return moe::launch_grouped_int8(d, stream);
+}
+
+moe_status check_int8_weights(const Int8Weights& w) {
+    MOE_TRY(check_ptr(w.gate, "w_gate"));
+    MOE_TRY(check_ptr(w.s_gate, "s_gate"));
+    MOE_TRY(check_ptr(w.up, "w_up"));
+    MOE_TRY(check_ptr(w.s_up, "s_up"));
+    MOE_TRY(check_ptr(w.down, "w_down"));
+    return check_ptr(w.s_down, "s_down");
+}
+
+}  // namespace
+
+MOE_EXPORT size_t moe_int8_workspace_bytes(const moe_problem* p) {
+    if (check_problem(p) != MOE_OK) return 0;
+    return int8_layout(*p).total;
+}
+
+MOE_EXPORT moe_status moe_expert_ffn_int8(const moe_problem* p, const moe_bf16* x,
+                                          const int32_t* sorted_pairs,
+                                          const int32_t* expert_offsets, const int8_t* w_gate,
+                                          const float* s_gate, const int8_t* w_up,
+                                          const float* s_up, const int8_t* w_down,
+                                          const float* s_down, float* y, void* ws, size_t ws_bytes,
+                                          hipStream_t stream) {
+    MOE_TRY(check_problem(p));
+    if (p->T == 0) return ok();
+    const Int8Weights w{w_gate, w_up, w_down, s_gate, s_up, s_down};
+    MOE_TRY(check_ptr(x, "x"));
+    MOE_TRY(check_ptr(sorted_pairs, "sorted_pairs"));
+    MOE_TRY(check_ptr(expert_offsets, "expert_offsets"));
+    MOE_TRY(check_int8_weights(w));
+    MOE_TRY(check_ptr(y, "y"));
+    MOE_TRY(check_ws_bytes(int8_layout(*p).total, ws, ws_bytes));
+    return hip_status(run_ffn_int8(*p, x, sorted_pairs, expert_offsets, w, y, ws, stream),
+                      "int8 expert ffn launch");
+}
+
+MOE_EXPORT moe_status moe_forward_int8(const moe_problem* p, const moe_bf16* x,
+                                       const moe_bf16* w_router, const float* bias,
+                                       const int8_t* w_gate, const float* s_gate,
+                                       const int8_t* w_up, const float* s_up,
+                                       const int8_t* w_down, const float* s_down, void* out,
+                                       moe_dtype out_dtype, int32_t* topk_ids,
+                                       float* topk_weights, float* y, void* ws, size_t ws_bytes,
+                                       hipStream_t stream) {
+    MOE_TRY(check_problem(p));
+    if (out_dtype != MOE_DTYPE_F32 && out_dtype != MOE_DTYPE_BF16)
+        return fail(MOE_ERR_INVALID_ARG, "out_dtype=%d is not MOE_DTYPE_F32/BF16", (int)out_dtype);
+    if (p->T == 0) return ok();
+    const Int8Weights w{w_gate, w_up, w_down, s_gate, s_up, s_down};
+    MOE_TRY(check_ptr(x, "x"));
+    MOE_TRY(check_ptr(w_router, "w_router"));
+    MOE_TRY(check_ptr(bias, "bias", true));
+    MOE_TRY(check_int8_weights(w));
+    MOE_TRY(check_ptr(out, "out"));
+    MOE_TRY(check_ptr(topk_ids, "topk_ids", true));
+    MOE_TRY(check_ptr(topk_weights, "topk_weights", true));
+    MOE_TRY(check_ptr(y, "y"));
+    MOE_TRY(check_ws_bytes(int8_layout(*p).total, ws, ws_bytes));
+    const Layout L = layout_of(*p);
+    const moe::Problem q = to_internal(*p);
+    int32_t* ids = topk_ids ? topk_ids : at<int32_t>(ws, L.ids);
+    float* wts = topk_weights ? topk_weights : at<float>(ws, L.weights);
+    int32_t* off = at<int32_t>(ws, L.offsets);
+    int32_t* sorted = at<int32_t>(ws, L.sorted);
+    int32_t* rows = at<int32_t>(ws, L.rows);
+    const size_t h_bytes = static_cast<size_t>(p->T) * static_cast<size_t>(p->k) *
+                           static_cast<size_t>(p->I) * 2;
+    hipError_t e = moe::launch_route_scratch(q, x, w_router, bias, ids, wts, at<uint16_t>(ws, L.h),
+                                             h_bytes, stream);
+    if (e != hipSuccess) return hip_status(e, "route launch");
+    e = moe::launch_permute(q, ids, off, sorted, rows, at<int32_t>(ws, L.counts), stream);
+    if (e != hipSuccess) return hip_status(e, "permute launch");
+    e = run_ffn_int8(*p, x, sorted, off, w, y, ws, stream);
+    if (e != hipSuccess) return hip_status(e, "int8 expert ffn launch");
+    e = moe::launch_combine(q, y, rows, wts, out, out_dtype == MOE_DTYPE_BF16, stream);
+    return hip_status(e, "combine launch");
+}
+
+MOE_EXPORT size_t moe_backward_workspace_bytes(const moe_problem* p) {
+    if (check_problem(p) != MOE_OK) return 0;
+    return backward_layout(*p).total;
+}
+
+MOE_EXPORT moe_status moe_expert_ffn_backward(const moe_problem* p, const moe_bf16* x,
+                                              const int32_t* sorted_pairs,
+                                              const int32_t* expert_offsets,
+                                              const moe_bf16* w_gate, const moe_bf16* w_up,
+                                              const moe_bf16* w_down, const moe_bf16* dy, float* dx,
+                                              void* dw_gate, void* dw_up, void* dw_down,
+                                              moe_dtype dw_dtype, int accumulate, void* ws,
+                                              size_t ws_bytes, hipStream_t stream) {
+    MOE_TRY(check_problem(p));
+    MOE_TRY(check_gemm_out(dw_dtype, accumulate));
+    const bool empty = p->T == 0;
+    MOE_TRY(check_ptr(x, "x", empty));
+    MOE_TRY(check_ptr(sorted_pairs, "sorted_pairs", empty));
+    MOE_TRY(check_ptr(expert_offsets, "expert_offsets", empty && p->E == 1));
+    MOE_TRY(check_ptr(w_gate, "w_gate"));
+    MOE_TRY(check_ptr(w_up, "w_up"));
+    MOE_TRY(check_ptr(w_down, "w_down"));
+    MOE_TRY(check_ptr(dy, "dy", empty));
+    MOE_TRY(check_ptr(dx, "dx", empty));
+    MOE_TRY(check_ptr(dw_gate, "dw_gate"));
+    MOE_TRY(check_ptr(dw_up, "dw_up"));
+    MOE_TRY(check_ptr(dw_down, "dw_down"));
+    const BackwardLayout L = backward_layout(*p);
+    MOE_TRY(check_ws_bytes(L.total, ws, ws_bytes));
+    const char* what = "expert ffn backward launch";
+    void* sums = at<char>(ws, L.sums);
+    // the products again: g, u = x . w^T and dh = dy . w_down, in fp32
+    moe::GemmArgs a = gemm_args(gate_shape(*p));
+    a.a = x;
+    a.pairs = sorted_pairs;
+    a.offsets = expert_offsets;
+    a.ws = sums;
+    moe::GemmArgs d = gemm_args(down_shape(*p));
+    d.offsets = expert_offsets;
+    d.ws = sums;
+    hipError_t e = hipSuccess;
+    if (!empty) {
+        a.w = w_gate;
+        a.out = at<float>(ws, L.g);
+        e = moe::launch_grouped_gemm(a, stream);
+        if (e != hipSuccess) return hip_status(e, what);
+        a.w = w_up;
+        a.out = at<float>(ws, L.u);
+        e = moe::launch_grouped_gemm(a, stream);
+        if (e != hipSuccess) return hip_status(e, what);
+        d.dout = dy;
+        d.w = w_down;
+        d.out = at<float>(ws, L.dh);
+        e = moe::launch_grouped_dgrad(d, stream);
+        if (e != hipSuccess) return hip_status(e, what);
+        e = moe::launch_swiglu_backward(at<float>(ws, L.g), at<float>(ws, L.u), at<float>(ws, L.dh), a.P * p->I,
+                                        at<uint16_t>(ws, L.h), at<uint16_t>(ws, L.dg), at<uint16_t>(ws, L.du),
+                                        stream);
+        if (e != hipSuccess) return hip_status(e, what);
+        // dx = dg . w_gate + du . w_up
+        a.dout = at<uint16_t>(ws, L.dg);
+        a.w = w_gate;
+        a.out = dx;
+        e = moe::launch_grouped_dgrad(a, stream);
+        if (e != hipSuccess) return hip_status(e, what);
+        a.dout = at<uint16_t>(ws, L.du);
+        a.w = w_up;
+        a.accumulate = true;
+        e = moe::launch_grouped_dgrad(a, stream);
+        if (e != hipSuccess) return hip_status(e, what);
+    }
+    a.out_bf16 = dw_dtype == MOE_DTYPE_BF16;
+    a.accumulate = accumulate != 0;
+    a.dout = at<uint16_t>(ws, L.dg);
+    a.out = dw_gate;
+    e = moe::launch_grouped_wgrad(a, stream);
+    if (e != hipSuccess) return hip_status(e, what);
+    a.dout = at<uint16_t>(ws, L.du);
+    a.out = dw_up;
+    e = moe::launch_grouped_wgrad(a, stream);
+    if (e != hipSuccess) return hip_status(e, what);
+    d.out_bf16 = a.out_bf16;
+    d.accumulate = a.accumulate;
+    d.dout = dy;
+    d.a = at<uint16_t>(ws, L.h);
+    d.out = dw_down;
+    return hip_status(moe::launch_grouped_wgrad(d, stream), what);
 }
 
 MOE_EXPORT const char* moe_status_string(moe_status s) {

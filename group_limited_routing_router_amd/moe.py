@@ -63,6 +63,8 @@ EXPORTS = ("moe_workspace_bytes", "moe_route", "moe_permute", "moe_expert_ffn",
            # grouped products (include/moe_gemm.h)
            "moe_gemm_workspace_bytes", "moe_grouped_gemm", "moe_grouped_gemm_dgrad",
            "moe_grouped_gemm_wgrad", "moe_quantize_rows_int8", "moe_grouped_gemm_int8",
+           "moe_int8_workspace_bytes", "moe_expert_ffn_int8", "moe_forward_int8",
+           "moe_backward_workspace_bytes", "moe_expert_ffn_backward",
            # measurement kernels (include/moe_peak.h)
            "moe_peak_stream_read", "moe_peak_mfma_bf16", "moe_peak_mfma_bf16_flops",
            "moe_peak_mfma_stream", "moe_peak_mfma_stream_flops", "moe_peak_mfma_stream_bytes")
@@ -145,6 +147,18 @@ def load_library():
         lib.moe_quantize_rows_int8.restype = st
         lib.moe_grouped_gemm_int8.argtypes = [gemm, P, P, P, P, P, P, P, i32, P, size, P]
         lib.moe_grouped_gemm_int8.restype = st
+        lib.moe_int8_workspace_bytes.argtypes = [prob]
+        lib.moe_int8_workspace_bytes.restype = size
+        lib.moe_expert_ffn_int8.argtypes = [prob, P, P, P, P, P, P, P, P, P, P, P, size, P]
+        lib.moe_expert_ffn_int8.restype = st
+        lib.moe_forward_int8.argtypes = [prob, P, P, P, P, P, P, P, P, P, P, i32, P, P, P, P, size,
+                                         P]
+        lib.moe_forward_int8.restype = st
+        lib.moe_backward_workspace_bytes.argtypes = [prob]
+        lib.moe_backward_workspace_bytes.restype = size
+        lib.moe_expert_ffn_backward.argtypes = [prob, P, P, P, P, P, P, P, P, P, P, P, i32, i32, P,
+                                                size, P]
+        lib.moe_expert_ffn_backward.restype = st
         lib.moe_peak_stream_read.argtypes = [P, ctypes.c_size_t, ctypes.c_int, P, ctypes.c_int, P]
         lib.moe_peak_stream_read.restype = st
         lib.moe_peak_mfma_bf16.argtypes = [ctypes.c_int64, ctypes.c_int, P, ctypes.c_int, P]
@@ -400,6 +414,70 @@ def moe_grouped_gemm_int8(g, a, a_scale, sorted_pairs, expert_offsets, w, w_scal
         _arg(expert_offsets, "expert_offsets", _I32, E + 1, dev, E == 1),
         _arg(w, "w", _I8, E * N * K, dev), _arg(w_scale, "w_scale", _F32, E * N, dev),
         _arg(out, "out", out.dtype, P * N, dev), _dtype_code(out), wp, wn, _on(stream, dev)))
+
+
+def moe_int8_workspace_bytes(p: MoEProblem) -> int:
+    return int(load_library().moe_int8_workspace_bytes(p))
+
+
+def _int8_weights(p, dev, q_gate, s_gate, q_up, s_up, q_down, s_down):
+    n, gate, down = p.E * p.I * p.H, p.E * p.I, p.E * p.H
+    return (_arg(q_gate, "q_gate", _I8, n, dev), _arg(s_gate, "s_gate", _F32, gate, dev),
+            _arg(q_up, "q_up", _I8, n, dev), _arg(s_up, "s_up", _F32, gate, dev),
+            _arg(q_down, "q_down", _I8, n, dev), _arg(s_down, "s_down", _F32, down, dev))
+
+
+def moe_expert_ffn_int8(p, x, sorted_pairs, expert_offsets, q_gate, s_gate, q_up, s_up, q_down,
+                        s_down, y, ws, stream=None):
+    """The experts in 8-bit integers: y [T*k,H] fp32 in sorted order."""
+    dev = torch.cuda.current_device()
+    P = p.T * p.k
+    wp, wn = _ws_args(ws, dev)
+    _check(load_library().moe_expert_ffn_int8(
+        p, _arg(x, "x", _BF16, p.T * p.H, dev), _arg(sorted_pairs, "sorted_pairs", _I32, P, dev),
+        _arg(expert_offsets, "expert_offsets", _I32, p.E + 1, dev),
+        *_int8_weights(p, dev, q_gate, s_gate, q_up, s_up, q_down, s_down),
+        _arg(y, "y", _F32, P * p.H, dev), wp, wn, _on(stream, dev)))
+
+
+def moe_forward_int8(p, x, w_router, bias, q_gate, s_gate, q_up, s_up, q_down, s_down, out,
+                     topk_ids, topk_weights, y, ws, stream=None):
+    """moe_forward with the experts in 8-bit integers."""
+    dev = torch.cuda.current_device()
+    P = p.T * p.k
+    wp, wn = _ws_args(ws, dev)
+    _check(load_library().moe_forward_int8(
+        p, _arg(x, "x", _BF16, p.T * p.H, dev), _arg(w_router, "w_router", _BF16, p.E * p.H, dev),
+        _arg(bias, "bias", _F32, p.E, dev, True),
+        *_int8_weights(p, dev, q_gate, s_gate, q_up, s_up, q_down, s_down),
+        _arg(out, "out", out.dtype, p.T * p.H, dev), _dtype_code(out),
+        _arg(topk_ids, "topk_ids", _I32, P, dev, True),
+        _arg(topk_weights, "topk_weights", _F32, P, dev, True), _arg(y, "y", _F32, P * p.H, dev),
+        wp, wn, _on(stream, dev)))
+
+
+def moe_backward_workspace_bytes(p: MoEProblem) -> int:
+    return int(load_library().moe_backward_workspace_bytes(p))
+
+
+def moe_expert_ffn_backward(p, x, sorted_pairs, expert_offsets, w_gate, w_up, w_down, dy, dx,
+                            dw_gate, dw_up, dw_down, ws, accumulate=False, stream=None):
+    """The gradients of moe_expert_ffn from dy [T*k,H] bf16: dx [T*k,H] fp32,
+    both in sorted order, and dw_gate, dw_up [E,I,H], dw_down [E,H,I] (fp32 or
+    bf16; += with accumulate)."""
+    dev = torch.cuda.current_device()
+    P, n, empty = p.T * p.k, p.E * p.I * p.H, p.T == 0
+    wp, wn = _ws_args(ws, dev)
+    _check(load_library().moe_expert_ffn_backward(
+        p, _arg(x, "x", _BF16, p.T * p.H, dev, empty),
+        _arg(sorted_pairs, "sorted_pairs", _I32, P, dev, empty),
+        _arg(expert_offsets, "expert_offsets", _I32, p.E + 1, dev, empty and p.E == 1),
+        _arg(w_gate, "w_gate", _BF16, n, dev), _arg(w_up, "w_up", _BF16, n, dev),
+        _arg(w_down, "w_down", _BF16, n, dev), _arg(dy, "dy", _BF16, P * p.H, dev, empty),
+        _arg(dx, "dx", _F32, P * p.H, dev, empty), _arg(dw_gate, "dw_gate", dw_gate.dtype, n, dev),
+        _arg(dw_up, "dw_up", dw_gate.dtype, n, dev),
+        _arg(dw_down, "dw_down", dw_gate.dtype, n, dev), _dtype_code(dw_gate),
+        1 if accumulate else 0, wp, wn, _on(stream, dev)))
 
 
 def moe_peak_stream_read(buf, sink, workgroups, nontemporal=False, stream=None):

@@ -106,6 +106,58 @@ moe_status moe_grouped_gemm_int8(const moe_gemm_problem* g, const int8_t* a, con
                                  moe_dtype out_dtype, void* ws, size_t ws_bytes,
                                  hipStream_t stream);
 
+/* ---- the experts of moe.h on these products ---- */
+
+/* Experts with int8 weights and activations (moe_expert_ffn, moe_forward).
+ * The rows of x are quantised as moe_quantize_rows_int8 does it, g and u are
+ * int8 products in fp32, h = silu(g) u in fp32 is quantised by rows in the
+ * same way (codes to the nearest of the fp32 quotient), y is an int8 product:
+ *     g[n] = sx s_gate[e,n] (xc . w_gate[e,n]),  u likewise,
+ *     y[m] = sh s_down[e,m] (hc . w_down[e,m])
+ *   w_gate, w_up  [E,I,H] int8 codes;  s_gate, s_up  [E,I] fp32
+ *   w_down        [E,H,I] int8 codes;  s_down        [E,H] fp32
+ *   ws            moe_int8_workspace_bytes(p) bytes
+ * A token that holds an infinity or NaN has NaN in its own outputs alone.
+ * Everything else as moe_expert_ffn / moe_forward. */
+size_t moe_int8_workspace_bytes(const moe_problem* p);
+
+moe_status moe_expert_ffn_int8(const moe_problem* p, const moe_bf16* x,
+                               const int32_t* sorted_pairs, const int32_t* expert_offsets,
+                               const int8_t* w_gate, const float* s_gate, const int8_t* w_up,
+                               const float* s_up, const int8_t* w_down, const float* s_down,
+                               float* y, void* ws, size_t ws_bytes, hipStream_t stream);
+
+moe_status moe_forward_int8(const moe_problem* p, const moe_bf16* x, const moe_bf16* w_router,
+                            const float* bias, const int8_t* w_gate, const float* s_gate,
+                            const int8_t* w_up, const float* s_up, const int8_t* w_down,
+                            const float* s_down, void* out, moe_dtype out_dtype, int32_t* topk_ids,
+                            float* topk_weights, float* y, void* ws, size_t ws_bytes,
+                            hipStream_t stream);
+
+/* The gradients of moe_expert_ffn (bf16 weights) from the gradient of y:
+ *   x, sorted_pairs, expert_offsets, w_gate, w_up, w_down  as the forward call
+ *   dy       [T*k,H] bf16 in sorted order
+ *   dx       [T*k,H] fp32 out in sorted order: the gradient of each pair's
+ *            row of x (the sum over a token's pairs is moe_combine with
+ *            weights and scale of one)
+ *   dw_gate, dw_up [E,I,H], dw_down [E,H,I]  out, fp32 or bf16 (dw_dtype);
+ *            zero for idle experts;  accumulate not 0: += (fp32 only)
+ *   ws       moe_backward_workspace_bytes(p) bytes
+ * g, u (the products of the forward pass, computed again) and dh = dy . w_down
+ * are fp32; h = silu(g) u, dg = dh u s (1 + g (1 - s)) and du = dh g s, with s
+ * = 1 / (1 + exp(-g)), are rounded to bf16 and multiplied:
+ *     dw_down = dy^T h, dw_gate = dg^T x, dw_up = du^T x (by expert),
+ *     dx = dg . w_gate + du . w_up
+ * With T = 0 the weight gradients are still written. */
+size_t moe_backward_workspace_bytes(const moe_problem* p);
+
+moe_status moe_expert_ffn_backward(const moe_problem* p, const moe_bf16* x,
+                                   const int32_t* sorted_pairs, const int32_t* expert_offsets,
+                                   const moe_bf16* w_gate, const moe_bf16* w_up,
+                                   const moe_bf16* w_down, const moe_bf16* dy, float* dx,
+                                   void* dw_gate, void* dw_up, void* dw_down, moe_dtype dw_dtype,
+                                   int accumulate, void* ws, size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

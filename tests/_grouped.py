@@ -38,10 +38,12 @@ def problem(P, S, E, N, K, k=1):
 
 
 class Case:
-    """Inputs of every grouped product of one shape, on the CPU: P positions
-    of which the first `first` and the last `behind` belong to no expert."""
+    """Inputs of every grouped product of one shape: P positions of which the
+    first `first` and the last `behind` belong to no expert.  The references
+    are computed on `device`."""
 
-    def __init__(self, P, E, N, K, k=1, kind="random", seed=0, first=0, behind=0, S=None):
+    def __init__(self, P, E, N, K, k=1, kind="random", seed=0, first=0, behind=0, S=None,
+                 device="cpu"):
         rng = np.random.default_rng(seed)
         gen = torch.Generator().manual_seed(seed)
         self.P, self.E, self.N, self.K, self.k = P, E, N, K, k
@@ -61,6 +63,8 @@ class Case:
         self.w8 = torch.randint(-128, 128, (E, N, K), generator=gen, dtype=torch.int8)
         self.a_scale = torch.rand((self.S,), generator=gen) * 0.05 + 1e-3
         self.w_scale = torch.rand((E, N), generator=gen) * 0.01 + 1e-4
+        for name in ("a", "w", "dout", "a8", "w8", "a_scale", "w_scale", "rows"):
+            setattr(self, name, getattr(self, name).to(device))
 
     def problem(self):
         return problem(self.P, self.S, self.E, self.N, self.K, self.k)
@@ -76,7 +80,7 @@ class Case:
 
     # each reference: (value, sum of magnitudes, length of the sum) in 64 bits
     def product(self):
-        v = torch.zeros((self.P, self.N), dtype=torch.float64)
+        v = torch.zeros((self.P, self.N), dtype=torch.float64, device=self.a.device)
         m = torch.zeros_like(v)
         for e, i, j in self.spans():
             a, w = self.a[self.rows[i:j]].double(), self.w[e].double()
@@ -85,7 +89,7 @@ class Case:
         return v, m, self.K
 
     def input_grad(self):
-        v = torch.zeros((self.P, self.K), dtype=torch.float64)
+        v = torch.zeros((self.P, self.K), dtype=torch.float64, device=self.a.device)
         m = torch.zeros_like(v)
         for e, i, j in self.spans():
             d, w = self.dout[i:j].double(), self.w[e].double()
@@ -94,7 +98,7 @@ class Case:
         return v, m, self.N
 
     def weight_grad(self):
-        v = torch.zeros((self.E, self.N, self.K), dtype=torch.float64)
+        v = torch.zeros((self.E, self.N, self.K), dtype=torch.float64, device=self.a.device)
         m = torch.zeros_like(v)
         for e, i, j in self.spans():
             d, a = self.dout[i:j].double(), self.a[self.rows[i:j]].double()
@@ -105,7 +109,7 @@ class Case:
     def int8(self):
         """The int8 product exactly as defined: an exact sum, rounded to fp32,
         times the fp32 product of the scales."""
-        v = torch.zeros((self.P, self.N), dtype=torch.float32)
+        v = torch.zeros((self.P, self.N), dtype=torch.float32, device=self.a.device)
         for e, i, j in self.spans():
             acc = self.a8[self.rows[i:j]].double() @ self.w8[e].double().T
             v[i:j] = acc.float() * (self.a_scale[self.rows[i:j]][:, None] * self.w_scale[e][None, :])

@@ -53,6 +53,8 @@ def run(moe, c, op, dtype, offsets=True, accumulate=None, stream=None):
 
 def check(c, op, dtype, got, start=None):
     own = c.owned()
+    got = got.to(c.a.device)
+    own = own.to(c.a.device)
     if op == "int8":
         ref = c.int8().to(dtype)
         assert torch.equal(got[own], ref[own]), f"{int((got[own] != ref[own]).sum())} values differ"
@@ -62,7 +64,7 @@ def check(c, op, dtype, got, start=None):
             ref = ref + start.double()
         tol = tolerance(ref, mag, length, dtype, start)
         if op == "weight_grad":
-            own = torch.ones(c.E, dtype=torch.bool)
+            own = torch.ones(c.E, dtype=torch.bool, device=got.device)
         w = worst(got[own], ref[own], tol[own])
         assert w <= 1.0, f"error {w:.3g} of the tolerance"
     if op != "weight_grad" and start is None:
@@ -102,6 +104,21 @@ def test_against_64_bits(moe, shape, op, dtype):
     P, E, N, K, k, kind = shape
     print(f"[case] {op} {shape} {dtype}", flush=True)
     c = Case(P, E, N, K, k, kind, seed=P + N)
+    check(c, op, dtype, run(moe, c, op, dtype))
+
+
+@pytest.mark.parametrize("op", ["product", "input_grad", "weight_grad", "int8"])
+@pytest.mark.parametrize("shape,dtype", [
+    ((9000, 8, 4096, 1008, 1), torch.bfloat16),   # many tiles: 256 rows each
+    ((4500, 8, 1008, 4096, 2), torch.float32),
+    ((1000, 256, 1040, 1024, 4), torch.bfloat16),  # a large weight stream and few rows
+    ((7000, 256, 1040, 1024, 1), torch.float32),
+    ((12000, 256, 1040, 1024, 8), torch.bfloat16),
+], ids=lambda s: "P%d_E%d_N%d_K%d_k%d" % s if isinstance(s, tuple) else str(s).split(".")[1])
+def test_large(moe, shape, dtype, op):
+    """The tiles and weight streams of larger shapes (references on the GPU)."""
+    print(f"[case] {op} {shape} {dtype}", flush=True)
+    c = Case(*shape, kind="random", seed=shape[0], first=3, behind=9, device="cuda")
     check(c, op, dtype, run(moe, c, op, dtype))
 
 
