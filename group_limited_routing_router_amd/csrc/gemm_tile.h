@@ -369,17 +369,26 @@ __global__ __launch_bounds__(kThreads, (TileShape<BX, BY>::kPerCu)) void gemm_ti
     const bool out_bf16 = g.out_bf16 && !split, accumulate = g.accumulate && !split;
     void* const out =
         split ? static_cast<float*>(g.ws) + static_cast<int64_t>(blockIdx.y) * g.P * cols : static_cast<float*>(g.out);
+    // int8: the scales of this lane's rows, all asked for at once
+    float a_sc[YB];
+    if constexpr (I8) {
+        int64_t src[YB];
+#pragma unroll
+        for (int m = 0; m < YB; ++m) {
+            const int64_t q = orow0 + min((wy + WY * m) * 32 + r32, rows - 1);
+            src[m] = GATHER ? g.pairs[q] : q;
+        }
+#pragma unroll
+        for (int m = 0; m < YB; ++m) {
+            int64_t s = GATHER ? static_cast<int32_t>(src[m]) / g.k : src[m];
+            s = s < 0 ? 0 : (s >= g.S ? g.S - 1 : s);
+            a_sc[m] = g.a_scale[s];
+        }
+    }
 #pragma unroll
     for (int m = 0; m < YB; ++m) {
         if (m >= valid_blocks) continue;
         const int blk = wy + WY * m;
-        float a_sc = 0.0f;
-        if constexpr (I8) {
-            const int64_t q = orow0 + min(blk * 32 + r32, rows - 1);
-            int64_t s = GATHER ? g.pairs[q] / g.k : q;
-            s = s < 0 ? 0 : (s >= g.S ? g.S - 1 : s);
-            a_sc = g.a_scale[s];
-        }
 #pragma unroll
         for (int n = 0; n < XB; ++n)
 #pragma unroll
@@ -396,7 +405,7 @@ __global__ __launch_bounds__(kThreads, (TileShape<BX, BY>::kPerCu)) void gemm_ti
                     const int at = min(wc0 + col, cols - 4);
                     const f32x4 ws = *reinterpret_cast<const f32x4*>(g.w_scale + static_cast<int64_t>(e) * N + at);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = static_cast<float>(acc[m][n][4 * i4 + i]) * (a_sc * ws[i]);
+                    for (int i = 0; i < 4; ++i) v[i] = static_cast<float>(acc[m][n][4 * i4 + i]) * (a_sc[m] * ws[i]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) v[i] = acc[m][n][4 * i4 + i];

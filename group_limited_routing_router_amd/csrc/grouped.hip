@@ -6,6 +6,8 @@
 //   input grad   da[q,k]   = sum_n dout[q,n] w[e,n,k]
 //   weight grad  dw[e,n,k] = sum_{q of e} dout[q,n] a[row(q),k]
 //   int8         out[q,n]  = a_scale[row(q)] w_scale[e,n] sum_k a[row(q),k] w[e,n,k]
+#include <math.h>
+
 #include "common.h"
 #include "gemm_tile.h"
 #include "gemm_wgrad.h"
@@ -197,16 +199,21 @@ struct TilePlan {
     int splits;  // parts of the reduction
 };
 
-// Microseconds of `tiles` workgroups over `stages` stages each: a round holds
-// one 256-row tile on each compute unit or two of the smaller ones, and costs
-// about 4 us beside its stages (measured: a stage of 128 bytes takes 1.85 us on
-// 256 rows; 0.6 us on 128 and 0.22 us on 32 with a compute unit to itself, 1.1
-// and 0.45 us with two on it).
+// Microseconds of `tiles` workgroups over `stages` stages each.  A round holds
+// one 256-row tile on each compute unit or two of the smaller ones.  Measured:
+// a stage (128 bytes of reduction) takes 1.85 us on 256 rows with the whole
+// chip busy, 1.05 with little of it; 0.6 on 128 and 0.22 on 32 rows with a
+// compute unit to itself, 1.1 and 0.45 with two on it; a round costs 11, 5.5
+// and 4 us beside its stages (first loads, writing out).
 float tile_time(int rows, float tiles, float stages) {
-    if (rows == 256) return (tiles > kNumCu ? tiles / kNumCu : 1.0f) * (1.85f * stages + 4.0f);
-    const float alone = rows == 128 ? 0.6f : 0.22f, paired = rows == 128 ? 1.1f : 0.45f;
-    if (tiles <= kNumCu) return alone * stages + 4.0f;
-    return (tiles > 2 * kNumCu ? tiles / (2 * kNumCu) : 1.0f) * (paired * stages + 4.0f);
+    const float slots = rows == 256 ? kNumCu : 2.0f * kNumCu;
+    float rounds = tiles / slots;
+    if (rounds < 4.0f) rounds = ceilf(rounds);
+    if (rows == 256)
+        return rounds * ((1.05f + 0.8f * (tiles < kNumCu ? tiles / kNumCu : 1.0f)) * stages + 11.0f);
+    const bool alone = tiles <= kNumCu;
+    if (rows == 128) return rounds * ((alone ? 0.6f : 1.1f) * stages + 5.5f);
+    return rounds * ((alone ? 0.22f : 0.45f) * stages + 4.0f);
 }
 
 // The host does not read the experts' counts: a mean expert is taken, with
@@ -215,19 +222,19 @@ template <int MODE, bool I8>
 TilePlan plan_tiles(const GemmArgs& g) {
     const int eb = I8 ? 1 : 2;
     const int cols = MODE == kProduct ? g.N : g.K;
-    const float mean_rows = static_cast<float>(g.P) / g.E;
-    const bool large = static_cast<int64_t>(g.E) * g.N * g.K * eb > kStreamBytes;
+    const int64_t met = g.E < g.P ? g.E : g.P;  // experts that can have rows
+    const float experts = static_cast<float>(met);
+    const float mean_rows = static_cast<float>(g.P) / experts;
+    const bool large = met * g.N * g.K * eb > kStreamBytes;
     const float stages = static_cast<float>(((MODE == kProduct ? g.K : g.N) + 128 / eb - 1) / (128 / eb));
     auto tiles_of = [&](int rows) {
-        const float experts = static_cast<float>(g.E < g.P ? g.E : g.P);
-        const float each = g.E == 1 ? static_cast<float>((g.P + rows - 1) / rows) : mean_rows / rows + 0.45f;
+        const float each = met == 1 ? static_cast<float>((g.P + rows - 1) / rows) : mean_rows / rows + 0.45f;
         const int width = rows == 256 ? 256 : 128;
         return experts * (each > 1.0f ? each : 1.0f) * static_cast<float>((cols + width - 1) / width);
     };
     TilePlan p{256, false, 1};
-    if (large && mean_rows > 32) return p;  // the fewest reads of the weights (4096 tokens, busy
-                                            // and idle experts: 1.46 against 1.68 ms on 128 rows)
-    if (large) {
+    const bool stream = large && mean_rows <= 32;
+    if (stream) {
         // the weight stream is the time: the tile that takes an expert's rows
         // at once and keeps the most loads in flight (256 experts of 2560 x
         // 5120: 4 rows each 0.97 ms on 32, 1.07 on 128 rows; 24 rows each 1.10
@@ -238,10 +245,14 @@ TilePlan plan_tiles(const GemmArgs& g) {
         p.nt = g.K * eb % 128 == 0;
     }
     float best = -1.0f;
+    // a large weight stream with more rows and tiles for every compute unit:
+    // the tile that reads the weights least often (4096 tokens over 256 busy
+    // and idle experts: 1.46 against 1.68 ms on 128 rows)
+    if (large && !stream && tiles_of(256) >= kNumCu) return p;
     for (int rows : {32, 128, 256}) {
-        if (large && rows != p.rows) continue;
-        for (int splits = 1; splits <= (rows == 256 ? 1 : 16); splits *= 2) {
-            if (splits > 1 && (stages < 4 * splits || large)) break;
+        if (stream && rows != p.rows) continue;
+        for (int splits = 1; splits <= 16; splits *= 2) {
+            if (splits > 1 && stages < 4 * splits) break;
             float t = tile_time(rows, tiles_of(rows) * splits, stages / splits);
             // the sums written and read, and one more launch
             if (splits > 1) t += 4.0f + 2.0f * splits * static_cast<float>(g.P) * cols * 4.0f / 5e6f;
@@ -308,9 +319,10 @@ template <int MODE, bool I8>
 hipError_t launch(const GemmArgs& g, hipStream_t s) {
     if (!gather_fits(g, I8 ? 1 : 2)) return launch_plain<MODE, I8>(g, s);
     const TilePlan p = plan_tiles<MODE, I8>(g);
-    if (p.rows == 256) return launch_tiles<MODE, I8, 256, 256>(g, s);
     hipError_t err;
-    if (p.rows == 32)
+    if (p.rows == 256)
+        err = launch_tiles<MODE, I8, 256, 256>(g, s, p.splits);
+    else if (p.rows == 32)
         err = p.nt ? launch_tiles<MODE, I8, 128, 32, true>(g, s, p.splits)
                    : launch_tiles<MODE, I8, 128, 32>(g, s, p.splits);
     else
@@ -335,12 +347,24 @@ WgradPlan plan_wgrad(const GemmArgs& g) {
     // 2560 x 5120, 256 rows each: 2.6 against 3.5 ms; 24 experts of 776 x
     // 1000 make 384 of them: 43 us on 1344 smaller ones)
     WgradPlan p{static_cast<int64_t>((g.K + 255) / 256) * ((g.N + 255) / 256) * g.E >= 512, 1};
-    const int64_t tiles = static_cast<int64_t>((g.K + 127) / 128) * ((g.N + 127) / 128) * g.E;
-    if (!p.big && tiles <= 256 && g.P / g.E >= 512) {
-        int64_t n = 512 / tiles;
-        if (n > g.P / g.E / 256) n = g.P / g.E / 256;
-        if (n > kMaxE / g.E) n = kMaxE / g.E;  // the kernel's list of parts
-        if (n > 1) p.splits = static_cast<int>(n);
+    if (p.big) return p;
+    // Parts of the positions, where the sums are long.  Microseconds: a stage
+    // of 32 positions takes 0.43 on two tiles to a compute unit, a tile about
+    // 16 stages more for its writing; the busiest expert is taken as three
+    // times the mean; the parts' sums are written, read and joined.
+    const float stages = static_cast<float>(g.P) / g.E / 32.0f;
+    const float tiles = static_cast<float>((g.K + 127) / 128) * static_cast<float>((g.N + 127) / 128) * g.E;
+    const float bytes = static_cast<float>(g.E) * g.N * g.K * 4.0f;
+    float best = -1.0f;
+    for (int n = 1; n <= 64 && n * g.E <= kMaxE; n *= 2) {  // kMaxE: the kernel's list of parts
+        if (n > 1 && stages < 8.0f * n) break;
+        const float all = tiles * (stages + 16.0f * n) / (2 * kNumCu), longest = 3.0f * stages / n + 16.0f;
+        float t = 0.43f * (all > longest ? all : longest);
+        if (n > 1) t += 4.0f + 2.0f * n * bytes / 5e6f;
+        if (best < 0.0f || t < best) {
+            best = t;
+            p.splits = n;
+        }
     }
     return p;
 }
@@ -395,7 +419,7 @@ __device__ __forceinline__ int code_of(float x, float m, float inv) {
 
 // Rows of bf16 as 8-bit codes with one scale each, LANES lanes a row.  A row
 // is read once and stays in registers (CHUNKS 16-byte pieces a lane); CHUNKS =
-// 0 reads it twice (K > 8192).  Bound by memory: 8192 rows of 5120 (126 MB
+// 0 reads it twice (K > 16384).  Bound by memory: 8192 rows of 5120 (126 MB
 // read and written).
 template <int LANES, int CHUNKS>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const uint16_t* x, int64_t rows, int K,
@@ -509,12 +533,16 @@ hipError_t launch_quantize_rows(int64_t rows, int K, const uint16_t* x, int8_t* 
                                 hipStream_t s) {
     if (rows <= 0) return hipSuccess;
     const dim3 threads(kThreads), whole(static_cast<unsigned>(rows)), waves(static_cast<unsigned>((rows + 3) / 4));
-    if (K <= 512)
+    if (rows < 2048 && K > 512 && K <= 2048)  // few rows: a workgroup each (301 rows of 2000: 3.4 against 5.5 us)
+        quantize_rows_kernel<kThreads, 1><<<whole, threads, 0, s>>>(x, rows, K, codes, scales);
+    else if (K <= 512)
         quantize_rows_kernel<kWave, 1><<<waves, threads, 0, s>>>(x, rows, K, codes, scales);
     else if (K <= 2048)
         quantize_rows_kernel<kWave, 4><<<waves, threads, 0, s>>>(x, rows, K, codes, scales);
     else if (K <= 8192)
         quantize_rows_kernel<kThreads, 4><<<whole, threads, 0, s>>>(x, rows, K, codes, scales);
+    else if (K <= 16384)
+        quantize_rows_kernel<kThreads, 8><<<whole, threads, 0, s>>>(x, rows, K, codes, scales);
     else
         quantize_rows_kernel<kThreads, 0><<<whole, threads, 0, s>>>(x, rows, K, codes, scales);
     return hipGetLastError();

@@ -90,6 +90,8 @@ SHAPES = [
     (5, 1, 128, 4112, 1, "even"),       # split reductions: the product's
     (40, 2, 192, 2064, 2, "random"),
     (3, 1, 2064, 128, 1, "even"),       # ... the input gradient's
+    (4400, 3, 4112, 144, 1, "random"),
+    (4400, 3, 160, 4112, 2, "random"),
     (70, 2, 3088, 144, 1, "random"),
     (2500, 2, 144, 176, 1, "random"),   # ... the weight gradient's
     (1700, 1, 64, 80, 2, "even"),
@@ -239,7 +241,7 @@ def quantize_ref(x):
 
 
 @pytest.mark.parametrize("rows,K", [(1, 16), (3, 48), (17, 256), (130, 2064), (5, 5120), (2, 65536),
-                                    (4099, 128)])
+                                    (4099, 128), (2100, 1040), (20, 16384), (19, 8208)])
 def test_quantize_rows(moe, rows, K):
     print(f"[case] quantize {rows} x {K}", flush=True)
     gen = torch.Generator().manual_seed(rows + K)
