@@ -203,17 +203,21 @@ struct TilePlan {
 // one 256-row tile on each compute unit or two of the smaller ones.  Measured:
 // a stage (128 bytes of reduction) takes 1.85 us on 256 rows with the whole
 // chip busy, 1.05 with little of it; 0.6 on 128 and 0.22 on 32 rows with a
-// compute unit to itself, 1.1 and 0.45 with two on it; a round costs 11, 5.5
+// compute unit to itself, 1.1 and 0.5 with two on it; a round costs 11, 5.5
 // and 4 us beside its stages (first loads, writing out).
 float tile_time(int rows, float tiles, float stages) {
     const float slots = rows == 256 ? kNumCu : 2.0f * kNumCu;
     float rounds = tiles / slots;
-    if (rounds < 4.0f) rounds = ceilf(rounds);
+    // the last round of a few is not full, but then runs faster
+    if (rounds <= 2.0f)
+        rounds = ceilf(rounds);
+    else if (rounds < 4.0f)
+        rounds = 0.5f * (rounds + ceilf(rounds));
     if (rows == 256)
         return rounds * ((1.05f + 0.8f * (tiles < kNumCu ? tiles / kNumCu : 1.0f)) * stages + 11.0f);
     const bool alone = tiles <= kNumCu;
     if (rows == 128) return rounds * ((alone ? 0.6f : 1.1f) * stages + 5.5f);
-    return rounds * ((alone ? 0.22f : 0.45f) * stages + 4.0f);
+    return rounds * ((alone ? 0.22f : 0.5f) * stages + 4.0f);
 }
 
 // The host does not read the experts' counts: a mean expert is taken, with
@@ -253,9 +257,13 @@ TilePlan plan_tiles(const GemmArgs& g) {
         if (stream && rows != p.rows) continue;
         for (int splits = 1; splits <= 16; splits *= 2) {
             if (splits > 1 && stages < 4 * splits) break;
-            float t = tile_time(rows, tiles_of(rows) * splits, stages / splits);
+            // rows that are not whole lines take more lines a stage, which
+            // shows most where the tile's part of a row is short (185 x 4
+            // rows, K 2232: 112 us on 128 rows, 76 on 256)
+            const float lines = g.K * eb % 128 == 0 ? 1.0f : (rows == 256 ? 1.1f : 1.3f);
+            float t = tile_time(rows, tiles_of(rows) * splits, lines * stages / splits);
             // the sums written and read, and one more launch
-            if (splits > 1) t += 4.0f + 2.0f * splits * static_cast<float>(g.P) * cols * 4.0f / 5e6f;
+            if (splits > 1) t = 1.05f * t + 4.0f + 2.0f * splits * static_cast<float>(g.P) * cols * 4.0f / 5e6f;
             if (best < 0.0f || t < best) {
                 best = t;
                 p.rows = rows;
