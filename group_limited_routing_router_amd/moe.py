@@ -336,7 +336,11 @@ def _on(stream, device):
     """The handle of `stream` (the current one of the device if None)."""
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+    if isinstance(stream, int):
+        return stream
+    if stream.device.index != device:
+        raise ValueError(f"stream is on {stream.device}, not on the current GPU")
+    return stream.cuda_stream
 
 
 def moe_gemm_workspace_bytes(g: MoEGemmProblem) -> int:

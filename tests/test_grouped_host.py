@@ -180,6 +180,12 @@ def test_binding_checks(monkeypatch):
         moe.moe_grouped_gemm(g, a, None, None, w, out)
     with pytest.raises(ValueError):
         moe.moe_quantize_rows_int8(a.reshape(-1), torch.zeros(64 * 48, dtype=torch.int8), torch.zeros(64))
+
+    class OtherStream:
+        device = torch.device("cuda", 1)
+        cuda_stream = 0
+    with pytest.raises(ValueError):
+        moe.moe_grouped_gemm(g, a, None, off, w, out, stream=OtherStream())
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     with pytest.raises(ValueError):
         moe.moe_grouped_gemm(g, a, None, off, w, out)
