@@ -84,12 +84,10 @@ __device__ bool find_tile(const int32_t* offsets, int64_t P, int E, int ncol_til
         if (lane >= d) incl += v;
     }
     int32_t* s_wave_total = s_tstart + (kMaxE + 1);
-    if (lane == kWave - 1 && wave < kWaves) s_wave_total[wave] = incl;
+    if (lane == kWave - 1) s_wave_total[wave] = incl;
     __syncthreads();
-    if (tid < kMaxE) {  // larger workgroups: the waves past the experts only wait
-        for (int w = 0; w < wave; ++w) incl += s_wave_total[w];
-        s_tstart[tid + 1] = incl;  // exclusive prefix over positions; s_tstart[E] = total row tiles
-    }
+    for (int w = 0; w < wave; ++w) incl += s_wave_total[w];
+    s_tstart[tid + 1] = incl;  // exclusive prefix over positions; s_tstart[E] = total row tiles
     if (tid == 0) s_tstart[0] = 0;
     __syncthreads();
     const int64_t total = static_cast<int64_t>(s_tstart[E]) * ncol_tiles;

@@ -35,7 +35,7 @@ def run(moe, c, op, dtype, offsets=True, accumulate=None, stream=None):
     ws = ws_for(moe, g)
     shape = {"input_grad": (c.P, c.K), "weight_grad": (c.E, c.N, c.K)}.get(op, (c.P, c.N))
     out = (torch.full(shape, float("nan"), dtype=dtype, device="cuda") if accumulate is None
-           else accumulate.cuda())
+           else accumulate.clone())
     acc = accumulate is not None
     if op == "product":
         moe.moe_grouped_gemm(g, dev(c.a), dev(c.pairs), off, dev(c.w), out, ws, stream=stream)
@@ -162,13 +162,13 @@ def test_one_group_without_offsets(moe, op, P, N, K):
 
 @pytest.mark.parametrize("op", ["input_grad", "weight_grad"])
 @pytest.mark.parametrize("shape", [(60, 4, 72, 40, 1), (700, 3, 272, 320, 2), (9, 1, 640, 768, 1),
-                                   (6, 1, 2056, 72, 1), (1500, 1, 72, 80, 2)],
+                                   (6, 1, 2056, 72, 1), (1500, 1, 72, 80, 2), (4500, 8, 1008, 4096, 2)],
                          ids=lambda s: "P%d_E%d_N%d_K%d_k%d" % s)
 def test_accumulate(moe, op, shape):
     print(f"[case] {op} {shape}", flush=True)
-    c = Case(*shape, kind="random", seed=8)
+    c = Case(*shape, kind="random", seed=8, device="cuda")
     out = (c.P, c.K) if op == "input_grad" else (c.E, c.N, c.K)
-    start = torch.randn(out, generator=torch.Generator().manual_seed(1))
+    start = torch.randn(out, generator=torch.Generator().manual_seed(1)).cuda()
     check(c, op, torch.float32, run(moe, c, op, torch.float32, accumulate=start), start)
 
 
