@@ -5,6 +5,7 @@
 #include <type_traits>
 
 #include "common.h"
+#include "schedule.h"
 
 namespace moe {
 namespace {
@@ -72,7 +73,7 @@ __device__ bool find_tile(const int32_t* offsets, int64_t P, int E, int ncol_til
     if (tid < E) {
         const int ex = expert_at(tid);
         const int n = s_off[ex + 1] - s_off[ex];
-        cnt = n > 0 ? (n + BM - 1) / BM : 0;
+        cnt = row_tiles_of(n, BM);
     }
     // inclusive prefix sum over positions (kThreads == kMaxE): within each
     // wave by shuffles, then the totals of the waves before it
@@ -125,9 +126,8 @@ __device__ bool find_tile(const int32_t* offsets, int64_t P, int E, int ncol_til
         row0_out = s_off[e] + mt * base + (mt < extra ? mt : extra);
         rows_out = base + (mt < extra ? 1 : 0);
     } else {
-        // per <= BM since GRAN divides BM, so the last tile keeps >= 1 row
         static_assert(BM % GRAN == 0, "granule divides the tile");
-        const int per = ((n_e + tiles_e - 1) / tiles_e + GRAN - 1) / GRAN * GRAN;
+        const int per = rows_per_tile(n_e, tiles_e, GRAN);
         row0_out = s_off[e] + mt * per;
         rows_out = min(per, n_e - mt * per);
     }

@@ -1,0 +1,86 @@
+"""The grouped products at the limits of their documented sizes: positions close
+to 2^31.  The inputs are zeros but for a few rows, so the outputs of all other
+rows are zeros; the values are small whole numbers, so every sum is exact."""
+import numpy as np
+import pytest
+import torch
+
+from _grouped import problem
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def moe():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    from group_limited_routing_router_amd import moe as m
+    m.load_library()
+    yield m
+    torch.cuda.empty_cache()
+
+
+def ws_for(moe, g):
+    return torch.full((max(16, moe.moe_gemm_workspace_bytes(g)),), 0xFF, dtype=torch.uint8, device="cuda")
+
+
+def count_where(x, pred, rows=1 << 27):
+    """How many values of x satisfy pred, a slice of rows at a time."""
+    return sum(int(torch.count_nonzero(pred(x[i:i + rows]))) for i in range(0, len(x), rows))
+
+
+@pytest.mark.parametrize("op", ["product", "input_grad", "weight_grad", "int8"])
+@pytest.mark.parametrize("P", [(1 << 31) - 40000])
+def test_positions_near_the_limit(moe, P, op):
+    """Two experts, the second with all rows but seven."""
+    K = 16 if op == "int8" else 8
+    N = 8
+    print(f"[case] {op} P={P}", flush=True)
+    rng = np.random.default_rng(P % 1000)
+    at = np.unique(np.concatenate([[0, 6, 7, 8, 127, 128, P // 2, P - 65, P - 64, P - 2, P - 1],
+                                   rng.integers(0, P, 40)]))
+    at_gpu = torch.from_numpy(at).cuda()
+    e = torch.from_numpy((at >= 7).astype(np.int64)).cuda()
+    gen = torch.Generator(device="cuda").manual_seed(P % 1000)
+    whole = torch.int8 if op == "int8" else torch.bfloat16
+
+    def some(shape):
+        return torch.randint(-4, 5, shape, generator=gen, device="cuda")
+
+    def rows(width):
+        """[P, width] zeros with a few rows of whole numbers, and these rows."""
+        full, few = torch.zeros((P, width), dtype=whole, device="cuda"), some((len(at), width))
+        full[at_gpu] = few.to(whole)
+        return full, few.double()
+
+    off = torch.tensor([0, 7, P], dtype=torch.int32, device="cuda")
+    w = some((2, N, K))
+    g = problem(P, P, 2, N, K, 1)
+    ws = ws_for(moe, g)
+    if op == "weight_grad":
+        a, few_a = rows(K)
+        dout, few_d = rows(N)
+        dw = torch.full((2, N, K), float("nan"), device="cuda")
+        moe.moe_grouped_gemm_wgrad(g, dout, a, None, off, dw, ws)
+        torch.cuda.synchronize()
+        ref = torch.stack([few_d[e == i].T @ few_a[e == i] for i in range(2)])
+        assert torch.equal(dw.double(), ref)
+        return
+    if op == "input_grad":
+        x, few = rows(N)
+        out = torch.full((P, K), float("nan"), dtype=torch.bfloat16, device="cuda")
+        moe.moe_grouped_gemm_dgrad(g, x, off, w.to(whole), out, ws)
+        ref = torch.bmm(few[:, None, :], w.double()[e])[:, 0]
+    else:
+        x, few = rows(K)
+        out = torch.full((P, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+        ref = torch.bmm(w.double()[e], few[:, :, None])[:, :, 0]
+        if op == "int8":
+            moe.moe_grouped_gemm_int8(g, x, torch.ones(P, device="cuda"), None, off, w.to(whole),
+                                      torch.ones((2, N), device="cuda"), out, ws)
+        else:
+            moe.moe_grouped_gemm(g, x, None, off, w.to(whole), out, ws)
+    torch.cuda.synchronize()
+    ref = ref.float().to(torch.bfloat16)
+    assert torch.equal(out[at_gpu], ref)
+    assert count_where(out, torch.isnan) == 0
+    assert count_where(out, lambda t: t != 0) == int(torch.count_nonzero(ref))
