@@ -169,7 +169,7 @@ __global__ __launch_bounds__(kThreads, (WgradShape<BX, BY, GATHER>::kPerCu)) voi
         // the same in every lane (P < 2^31): kept in scalar registers
         c.first = __builtin_amdgcn_readfirstlane(static_cast<int>(b));
         c.red = __builtin_amdgcn_readfirstlane(static_cast<int>(m));
-        c.nk = (c.red + SR - 1) / SR;
+        c.nk = row_tiles_of(c.red, SR);
     };
     auto enter_tile = [&](Cursor& c) {
         const int band_tiles = kBand * col_tiles;

@@ -44,3 +44,11 @@ def test_rows_of_tiles(schedule, bm, gran):
 
 def test_no_rows(schedule):
     assert schedule.row_tiles_of(0, 128) == 0 and schedule.row_tiles_of(-5, 128) == 0
+
+
+def test_stages_of_the_weight_gradient(schedule):
+    """Its stages are 32 positions: the count holds up to the last position."""
+    for n in (1, 31, 32, 33, TOP - 31, TOP - 30, TOP):
+        assert schedule.row_tiles_of(n, 32) == (n + 31) // 32
+    src = open(os.path.join(CSRC, "gemm_wgrad.h")).read()
+    assert "c.nk = row_tiles_of(c.red, SR);" in src
