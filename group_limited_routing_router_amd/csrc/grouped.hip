@@ -162,20 +162,20 @@ hipError_t launch_plain(const GemmArgs& g, hipStream_t s) {
 
 // Workgroups of a tiled launch (an upper bound: the host does not read the
 // experts' counts).
-template <int MODE, int BX, int BY>
-int64_t tile_grid(const GemmArgs& g) {
+template <int MODE>
+int64_t tile_grid(const GemmArgs& g, int bx, int by) {
     const int64_t cols = MODE == kProduct ? g.N : g.K;
-    const int64_t row_tiles = (g.P + BY - 1) / BY + (g.E < g.P ? g.E : g.P);
-    const int64_t tiles = row_tiles * ((cols + BX - 1) / BX);
+    const int64_t row_tiles = (g.P + by - 1) / by + (g.E < g.P ? g.E : g.P);
+    const int64_t tiles = row_tiles * ((cols + bx - 1) / bx);
     return (tiles + kNumXcd - 1) / kNumXcd * kNumXcd;
 }
 
 // splits > 1: the reduction in that many parts, whose sums go to g.ws.
 template <int MODE, bool I8, int BX, int BY, bool NT = false>
 hipError_t launch_tiles(const GemmArgs& g, hipStream_t s, int splits = 1) {
-    const int64_t grid = tile_grid<MODE, BX, BY>(g);
+    const int64_t grid = tile_grid<MODE>(g, BX, BY);
     if (grid <= 0) return hipSuccess;
-    if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+    if (grid > kMaxWorkgroups) return hipErrorInvalidConfiguration;
     const dim3 blocks(static_cast<unsigned>(grid), splits), threads(kThreads);
     if constexpr (MODE == kProduct) {
         if (g.pairs) {
@@ -255,6 +255,9 @@ TilePlan plan_tiles(const GemmArgs& g) {
     if (large && !stream && tiles_of(256) >= kNumCu) return p;
     for (int rows : {32, 128, 256}) {
         if (stream && rows != p.rows) continue;
+        // more tiles than a launch takes (2^31 - 1 rows of width 8 on 128
+        // rows); outputs of up to kMaxOutputs always fit on 256
+        if (rows < 256 && tile_grid<MODE>(g, 128, rows) > kMaxWorkgroups) continue;
         for (int splits = 1; splits <= 16; splits *= 2) {
             if (splits > 1 && stages < 4 * splits) break;
             // rows that are not whole lines take more lines a stage, which

@@ -34,6 +34,14 @@ struct GemmArgs {
     int splits;              // weight gradient: parts of each expert's positions
 };
 
+// A launch takes fewer than 2^32 threads along x: workgroups of 256.
+constexpr int64_t kMaxWorkgroups = (1LL << 24) - 1;
+
+// Outputs of one grouped product, at most (512 GiB of bf16): with P <= 2^31 rows
+// of at most 65536 columns over at most 256 experts, the 256 x 256 tiles are at
+// most (P / 256 + 257) (cols / 256 + 1) <= 2^22 + 2^23 + 2^16 + 2^9.
+constexpr int64_t kMaxOutputs = 1LL << 38;
+
 // Pairs handled by one block of the counting sort.
 constexpr int kPermuteChunk = 4096;
 

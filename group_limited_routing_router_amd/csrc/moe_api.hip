@@ -503,6 +503,19 @@ moe_status check_rows(const moe_gemm_problem& g, const int32_t* sorted_pairs) {
     return check_ptr(sorted_pairs, "sorted_pairs", true);
 }
 
+// The outputs of a product of P rows and cols columns.
+moe_status check_outputs(int64_t P, int64_t cols) {
+    if (P * cols > moe::kMaxOutputs)
+        return fail(MOE_ERR_UNSUPPORTED, "%lld x %lld outputs > 2^38", (long long)P, (long long)cols);
+    return MOE_OK;
+}
+
+// The outputs of the experts' products ([P,I] and [P,H]).
+moe_status check_expert_outputs(const moe_problem& p) {
+    MOE_TRY(check_outputs(p.T * p.k, p.I));
+    return check_outputs(p.T * p.k, p.H);
+}
+
 moe_status check_offsets(const moe_gemm_problem& g, const int32_t* expert_offsets) {
     return check_ptr(expert_offsets, "expert_offsets", g.E == 1);
 }
@@ -564,6 +577,7 @@ MOE_EXPORT moe_status moe_grouped_gemm(const moe_gemm_problem* g, const moe_bf16
                                        const moe_bf16* w, void* out, moe_dtype out_dtype, void* ws,
                                        size_t ws_bytes, hipStream_t stream) {
     MOE_TRY(check_gemm(g, 8));
+    MOE_TRY(check_outputs(g->P, g->N));
     MOE_TRY(check_gemm_out(out_dtype, 0));
     MOE_TRY(check_rows(*g, sorted_pairs));
     if (g->P == 0) return ok();
@@ -588,6 +602,7 @@ MOE_EXPORT moe_status moe_grouped_gemm_dgrad(const moe_gemm_problem* g, const mo
                                              void* da, moe_dtype da_dtype, int accumulate, void* ws,
                                              size_t ws_bytes, hipStream_t stream) {
     MOE_TRY(check_gemm(g, 8));
+    MOE_TRY(check_outputs(g->P, g->K));
     MOE_TRY(check_gemm_out(da_dtype, accumulate));
     if (g->P == 0) return ok();
     MOE_TRY(check_offsets(*g, expert_offsets));
@@ -651,6 +666,7 @@ MOE_EXPORT moe_status moe_grouped_gemm_int8(const moe_gemm_problem* g, const int
                                             const float* w_scale, void* out, moe_dtype out_dtype,
                                             void* ws, size_t ws_bytes, hipStream_t stream) {
     MOE_TRY(check_gemm(g, 16));
+    MOE_TRY(check_outputs(g->P, g->N));
     MOE_TRY(check_gemm_out(out_dtype, 0));
     MOE_TRY(check_rows(*g, sorted_pairs));
     if (g->P == 0) return ok();
@@ -783,7 +799,7 @@ moe_status check_int8_weights(const Int8Weights& w) {
 }  // namespace
 
 MOE_EXPORT size_t moe_int8_workspace_bytes(const moe_problem* p) {
-    if (check_problem(p) != MOE_OK) return 0;
+    if (check_problem(p) != MOE_OK || check_expert_outputs(*p) != MOE_OK) return 0;
     return int8_layout(*p).total;
 }
 
@@ -795,6 +811,7 @@ MOE_EXPORT moe_status moe_expert_ffn_int8(const moe_problem* p, const moe_bf16* 
                                           const float* s_down, float* y, void* ws, size_t ws_bytes,
                                           hipStream_t stream) {
     MOE_TRY(check_problem(p));
+    MOE_TRY(check_expert_outputs(*p));
     if (p->T == 0) return ok();
     const Int8Weights w{w_gate, w_up, w_down, s_gate, s_up, s_down};
     MOE_TRY(check_ptr(x, "x"));
@@ -816,6 +833,7 @@ MOE_EXPORT moe_status moe_forward_int8(const moe_problem* p, const moe_bf16* x,
                                        float* topk_weights, float* y, void* ws, size_t ws_bytes,
                                        hipStream_t stream) {
     MOE_TRY(check_problem(p));
+    MOE_TRY(check_expert_outputs(*p));
     if (out_dtype != MOE_DTYPE_F32 && out_dtype != MOE_DTYPE_BF16)
         return fail(MOE_ERR_INVALID_ARG, "out_dtype=%d is not MOE_DTYPE_F32/BF16", (int)out_dtype);
     if (p->T == 0) return ok();
@@ -850,7 +868,7 @@ MOE_EXPORT moe_status moe_forward_int8(const moe_problem* p, const moe_bf16* x,
 }
 
 MOE_EXPORT size_t moe_backward_workspace_bytes(const moe_problem* p) {
-    if (check_problem(p) != MOE_OK) return 0;
+    if (check_problem(p) != MOE_OK || check_expert_outputs(*p) != MOE_OK) return 0;
     return backward_layout(*p).total;
 }
 
@@ -863,6 +881,7 @@ MOE_EXPORT moe_status moe_expert_ffn_backward(const moe_problem* p, const moe_bf
                                               moe_dtype dw_dtype, int accumulate, void* ws,
                                               size_t ws_bytes, hipStream_t stream) {
     MOE_TRY(check_problem(p));
+    MOE_TRY(check_expert_outputs(*p));
     MOE_TRY(check_gemm_out(dw_dtype, accumulate));
     const bool empty = p->T == 0;
     MOE_TRY(check_ptr(x, "x", empty));

@@ -38,7 +38,8 @@ extern "C" {
  *   E  experts, 1 <= E <= 256
  *   N, K  the weights are [E,N,K]; multiples of 8 (K of 16 for the int8
  *      product), at most 65536
- *   k  positions per activation row, >= 1: row(q) = sorted_pairs[q] / k */
+ *   k  positions per activation row, >= 1: row(q) = sorted_pairs[q] / k
+ * The outputs of one call, P N (P K for the input gradient), at most 2^38. */
 typedef struct moe_gemm_problem {
     int64_t P, S;
     int32_t E, N, K, k;
@@ -117,6 +118,7 @@ moe_status moe_grouped_gemm_int8(const moe_gemm_problem* g, const int8_t* a, con
  *   w_gate, w_up  [E,I,H] int8 codes;  s_gate, s_up  [E,I] fp32
  *   w_down        [E,H,I] int8 codes;  s_down        [E,H] fp32
  *   ws            moe_int8_workspace_bytes(p) bytes
+ * T k I and T k H at most 2^38 (so too for moe_expert_ffn_backward).
  * A token that holds an infinity or NaN has NaN in its own outputs alone.
  * Everything else as moe_expert_ffn / moe_forward. */
 size_t moe_int8_workspace_bytes(const moe_problem* p);

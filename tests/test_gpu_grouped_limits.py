@@ -29,7 +29,7 @@ def count_where(x, pred, rows=1 << 27):
 
 
 @pytest.mark.parametrize("op", ["product", "input_grad", "weight_grad", "int8"])
-@pytest.mark.parametrize("P", [(1 << 31) - 40000])
+@pytest.mark.parametrize("P", [(1 << 31) - 40000, (1 << 31) - 1])
 def test_positions_near_the_limit(moe, P, op):
     """Two experts, the second with all rows but seven."""
     K = 16 if op == "int8" else 8

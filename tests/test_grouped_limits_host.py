@@ -1,0 +1,43 @@
+"""Sizes past what a launch takes are refused on the host, before anything is
+enqueued."""
+import numpy as np
+import pytest
+
+from group_limited_routing_router_amd import moe
+
+TOP = (1 << 31) - 1
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return moe.load_library()
+
+
+@pytest.fixture(scope="module")
+def good():
+    raw = np.zeros(4096, np.uint8)
+    yield raw.ctypes.data + (-raw.ctypes.data) % 64
+    del raw
+
+
+def test_outputs_past_the_limit(lib, good):
+    wide = moe.MoEGemmProblem(TOP, TOP, 2, 136, 8, 1)      # P N > 2^38
+    n = 1 << 40
+    assert lib.moe_grouped_gemm(wide, good, None, good, good, good, 1, good, n, None) == 2
+    assert b"2^38" in lib.moe_last_error()
+    wide = moe.MoEGemmProblem(TOP, TOP, 2, 136, 16, 1)
+    assert lib.moe_grouped_gemm_int8(wide, good, good, None, good, good, good, good, 1, good, n, None) == 2
+    deep = moe.MoEGemmProblem(TOP, TOP, 2, 8, 136, 1)      # P K > 2^38
+    assert lib.moe_grouped_gemm_dgrad(deep, good, good, good, good, 1, 0, good, n, None) == 2
+    assert b"2^38" in lib.moe_last_error()
+
+
+def test_experts_past_the_limit(lib, good):
+    n = 1 << 50
+    for H, I in ((256, 64), (128, 192)):
+        p = moe.MoEProblem(TOP, H, I, 4, 1, 1, 1, 1.0)
+        assert moe.moe_int8_workspace_bytes(p) == 0 and moe.moe_backward_workspace_bytes(p) == 0
+        assert lib.moe_expert_ffn_int8(p, *(good,) * 10, good, n, None) == 2
+        assert b"2^38" in lib.moe_last_error()
+        assert lib.moe_forward_int8(p, good, good, None, *(good,) * 7, 0, None, None, good, good, n, None) == 2
+        assert lib.moe_expert_ffn_backward(p, *(good,) * 11, 0, 0, good, n, None) == 2
