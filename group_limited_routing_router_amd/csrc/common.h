@@ -48,6 +48,11 @@ __device__ __forceinline__ void wave_lds_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
+// This workgroup's place in a grid of folded_grid().
+__device__ __forceinline__ int64_t folded_index() {
+    return static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+}
+
 __device__ __forceinline__ float sigmoid_f32(float z) { return 1.0f / (1.0f + expf(-z)); }
 
 // silu(z) = z * sigmoid(z) in fp32 with the hardware exp2 and reciprocal

@@ -437,8 +437,8 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const uint16_t*
                                                                  int8_t* codes, float* scales) {
     __shared__ float s_max[kWaves];
     const int tid = threadIdx.x, lane = tid % LANES;
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads / LANES) + tid / LANES;
-    if (LANES == kWave && r >= rows) return;  // whole waves; with one row a workgroup there are no others
+    const int64_t r = folded_index() * (kThreads / LANES) + tid / LANES;
+    if (r >= rows) return;  // whole waves, or the whole workgroup of one row
     const uint16_t* row = x + r * K;
     // magnitudes as integers: in this order infinity and NaN come last
     uint32_t top = 0;
@@ -543,7 +543,7 @@ hipError_t launch_grouped_int8(const GemmArgs& g, hipStream_t s) { return launch
 hipError_t launch_quantize_rows(int64_t rows, int K, const uint16_t* x, int8_t* codes, float* scales,
                                 hipStream_t s) {
     if (rows <= 0) return hipSuccess;
-    const dim3 threads(kThreads), whole(static_cast<unsigned>(rows)), waves(static_cast<unsigned>((rows + 3) / 4));
+    const dim3 threads(kThreads), whole = folded_grid(rows), waves = folded_grid((rows + 3) / 4);
     if (rows < 2048 && K > 512 && K <= 2048)  // few rows: a workgroup each (301 rows of 2000: 3.4 against 5.5 us)
         quantize_rows_kernel<kThreads, 1><<<whole, threads, 0, s>>>(x, rows, K, codes, scales);
     else if (K <= 512)

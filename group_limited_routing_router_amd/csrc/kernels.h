@@ -37,6 +37,14 @@ struct GemmArgs {
 // A launch takes fewer than 2^32 threads along x: workgroups of 256.
 constexpr int64_t kMaxWorkgroups = (1LL << 24) - 1;
 
+// A grid of n workgroups of 256 (n <= 2^35), in rows of 2^20 where one launch
+// dimension does not take them; workgroup i is folded_index().
+inline dim3 folded_grid(int64_t n) {
+    constexpr int64_t kRow = 1 << 20;
+    return n <= kMaxWorkgroups ? dim3(static_cast<unsigned>(n))
+                               : dim3(static_cast<unsigned>(kRow), static_cast<unsigned>((n + kRow - 1) / kRow));
+}
+
 // Outputs of one grouped product, at most (512 GiB of bf16): with P <= 2^31 rows
 // of at most 65536 columns over at most 256 experts, the 256 x 256 tiles are at
 // most (P / 256 + 257) (cols / 256 + 1) <= 2^22 + 2^23 + 2^16 + 2^9.

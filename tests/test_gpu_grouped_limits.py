@@ -84,3 +84,29 @@ def test_positions_near_the_limit(moe, P, op):
     assert torch.equal(out[at_gpu], ref)
     assert count_where(out, torch.isnan) == 0
     assert count_where(out, lambda t: t != 0) == int(torch.count_nonzero(ref))
+
+
+@pytest.mark.parametrize("rows,K", [((1 << 26) + 3, 16), ((1 << 24) + 1, 2064)])
+def test_quantize_more_rows_than_one_launch_dimension(moe, rows, K):
+    """More workgroups than fit along one dimension of a launch; 4099 rows over
+    and over, so every row's codes are known from the 64-bit reference."""
+    from test_gpu_grouped import quantize_ref
+    print(f"[case] quantize {rows} x {K}", flush=True)
+    gen = torch.Generator().manual_seed(K)
+    few = torch.randn((4099, K), generator=gen) * torch.exp(3 * torch.randn((4099, 1), generator=gen))
+    few = few.to(torch.bfloat16)
+    rc, rs = (t.cuda() for t in quantize_ref(few))
+    few = few.cuda()
+    step = 4099 * 128
+    x = torch.empty((rows, K), dtype=torch.bfloat16, device="cuda")
+    for i in range(0, rows, step):
+        n = min(step, rows - i)
+        x[i:i + n] = few.repeat(128, 1)[:n]
+    codes = torch.full((rows, K), 99, dtype=torch.int8, device="cuda")
+    scales = torch.full((rows,), float("nan"), device="cuda")
+    moe.moe_quantize_rows_int8(x, codes, scales)
+    torch.cuda.synchronize()
+    rc, rs = rc.repeat(128, 1), rs.repeat(128)
+    for i in range(0, rows, step):
+        n = min(step, rows - i)
+        assert torch.equal(codes[i:i + n], rc[:n]) and torch.equal(scales[i:i + n], rs[:n]), i
