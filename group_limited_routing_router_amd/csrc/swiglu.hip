@@ -24,8 +24,8 @@ __global__ __launch_bounds__(kThreads) void swiglu_quantize_kernel(const float* 
                                                                    float* scales) {
     __shared__ float s_max[kThreads / kWave];
     __shared__ int s_bad[kThreads / kWave];
-    const int64_t q = blockIdx.x;
-    if (q < offsets[0] || q >= offsets[E]) return;
+    const int64_t q = folded_index();
+    if (q >= P || q < offsets[0] || q >= offsets[E]) return;
     const int tid = threadIdx.x;
     const float* gr = g + q * I;
     const float* ur = u + q * I;
@@ -102,7 +102,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(const float* 
                                                                    int64_t values, uint16_t* h, uint16_t* dg,
                                                                    uint16_t* du) {
     typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    const int64_t at = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * 4;
+    const int64_t at = (folded_index() * kThreads + threadIdx.x) * 4;
     if (at >= values) return;
     const f32x4 a = *reinterpret_cast<const f32x4*>(g + at), b = *reinterpret_cast<const f32x4*>(u + at),
                 d = *reinterpret_cast<const f32x4*>(dh + at);
@@ -124,7 +124,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(const float* 
 hipError_t launch_swiglu_quantize(const float* g, const float* u, int64_t P, int I, const int32_t* offsets, int E,
                                   int8_t* codes, float* scales, hipStream_t s) {
     if (P <= 0) return hipSuccess;
-    const dim3 grid(static_cast<unsigned>(P)), threads(kThreads);
+    const dim3 grid = folded_grid(P), threads(kThreads);
     if (I <= 4096)
         swiglu_quantize_kernel<4><<<grid, threads, 0, s>>>(g, u, P, I, offsets, E, codes, scales);
     else if (I <= 16384)
@@ -138,8 +138,7 @@ hipError_t launch_swiglu_backward(const float* g, const float* u, const float* d
                                   uint16_t* dg, uint16_t* du, hipStream_t s) {
     const int64_t blocks = (values / 4 + kThreads - 1) / kThreads;
     if (blocks <= 0) return hipSuccess;
-    if (blocks > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-    swiglu_backward_kernel<<<dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s>>>(g, u, dh, values, h, dg, du);
+    swiglu_backward_kernel<<<folded_grid(blocks), dim3(kThreads), 0, s>>>(g, u, dh, values, h, dg, du);
     return hipGetLastError();
 }
 

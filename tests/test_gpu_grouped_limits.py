@@ -110,3 +110,37 @@ def test_quantize_more_rows_than_one_launch_dimension(moe, rows, K):
     for i in range(0, rows, step):
         n = min(step, rows - i)
         assert torch.equal(codes[i:i + n], rc[:n]) and torch.equal(scales[i:i + n], rs[:n]), i
+
+
+def test_int8_experts_of_more_positions_than_one_launch_dimension(moe):
+    """2^24 + 8 positions: the rows of h quantised by a workgroup each.  4096
+    tokens over and over with the same experts, so the same y over and over."""
+    base, k, E, H, I = 4096, 8, 8, 128, 64
+    T = (1 << 21) + 1
+    print(f"[case] int8 experts, {T} tokens", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x0 = torch.randn((base, H), generator=gen, device="cuda").to(torch.bfloat16)
+    x = x0.repeat(T // base + 1, 1)[:T].contiguous()
+
+    def weights(*shape):
+        return (torch.randint(-127, 128, shape, generator=gen, dtype=torch.int8, device="cuda"),
+                torch.rand(shape[:2], generator=gen, device="cuda") * 1e-3 + 1e-3)
+    w = [t for shape in ((E, I, H), (E, I, H), (E, H, I)) for t in weights(*shape)]
+
+    def run(x):
+        """Every token goes to every expert: expert e's positions are the tokens in order."""
+        n = len(x)
+        p = moe.MoEProblem(n, H, I, E, 1, 1, k, 1.0)
+        pairs = (torch.arange(n, device="cuda", dtype=torch.int32)[None, :] * k
+                 + torch.arange(E, device="cuda", dtype=torch.int32)[:, None]).reshape(-1).contiguous()
+        off = torch.arange(E + 1, device="cuda", dtype=torch.int32) * n
+        ws = torch.empty((moe.moe_int8_workspace_bytes(p),), dtype=torch.uint8, device="cuda")
+        y = torch.full((n * k, H), float("nan"), device="cuda")
+        moe.moe_expert_ffn_int8(p, x, pairs, off, *w, y, ws)
+        torch.cuda.synchronize()
+        return y.view(E, n, H)
+    few, many = run(x0), run(x)
+    assert not bool(torch.isnan(few).any())
+    for i in range(0, T, base):
+        n = min(base, T - i)
+        assert torch.equal(many[:, i:i + n], few[:, :n]), i
