@@ -48,7 +48,8 @@ __global__ __launch_bounds__(kCombineMaxThreads) void combine_kernel(int64_t T, 
                                                            const int32_t* __restrict__ pair_rows,
                                                            const float* __restrict__ weights,
                                                            void* __restrict__ out, bool nt) {
-    const int64_t t = blockIdx.x;
+    const int64_t t = folded_index();
+    if (t >= T) return;
     int32_t row[K];
     float w[K];
 #pragma unroll
@@ -98,7 +99,8 @@ __global__ __launch_bounds__(kCombineMaxThreads) void combine_kernel(int64_t T, 
 template <int K>
 hipError_t launch_k(const Problem& p, const float* y, const int32_t* pair_rows,
                     const float* weights, void* out, bool out_bf16, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(p.T)), block(combine_threads(p.H));
+    const int threads = combine_threads(p.H);
+    const dim3 grid = folded_grid(p.T, threads), block(threads);
     const bool nt = p.T * p.k * static_cast<int64_t>(p.H) * 4 > kStreamBytes;
     if (out_bf16)
         combine_kernel<K, true><<<grid, block, 0, s>>>(p.T, p.H, p.scale, y, pair_rows, weights, out, nt);
@@ -125,7 +127,8 @@ __global__ __launch_bounds__(kCombineMaxThreads) void combine_residual_kernel(
     bool nt) {
     __shared__ float s_part[kCombineMaxThreads / 64];
     const int nth = blockDim.x;
-    const int64_t t = blockIdx.x;
+    const int64_t t = folded_index();
+    if (t >= T) return;
     int32_t row[K];
     float w[K];
 #pragma unroll
@@ -194,7 +197,7 @@ hipError_t launch_residual_k(const Problem& p, const float* y, const int32_t* pa
     // 6.4 us at 128 tokens); otherwise 256 threads, whose shorter wait at the
     // barrier wins with many tokens (640 were 8% slower at 8192)
     const int threads = p.T < kWideBelowTokens ? combine_threads(p.H) : kThreads;
-    const dim3 grid(static_cast<unsigned>(p.T)), block(threads);
+    const dim3 grid = folded_grid(p.T, threads), block(threads);
     const int chunks = (p.H / 4 + threads - 1) / threads;
     const bool nt = p.T * p.k * static_cast<int64_t>(p.H) * 4 > kStreamBytes;
 #define MOE_RES(NC)                                                                       \

@@ -34,15 +34,18 @@ struct GemmArgs {
     int splits;              // weight gradient: parts of each expert's positions
 };
 
-// A launch takes fewer than 2^32 threads along x: workgroups of 256.
+// A launch takes fewer than 2^32 threads along x (the runtime wraps a longer
+// grid without an error): workgroups of 256.
 constexpr int64_t kMaxWorkgroups = (1LL << 24) - 1;
 
-// A grid of n workgroups of 256 (n <= 2^35), in rows of 2^20 where one launch
-// dimension does not take them; workgroup i is folded_index().
-inline dim3 folded_grid(int64_t n) {
+// A grid of n workgroups (n <= 2^35) of at most 1024 threads, in rows of 2^20
+// where one launch dimension does not take them; workgroup i is folded_index(),
+// up to a row less one of which are past n.
+inline dim3 folded_grid(int64_t n, int threads = 256) {
     constexpr int64_t kRow = 1 << 20;
-    return n <= kMaxWorkgroups ? dim3(static_cast<unsigned>(n))
-                               : dim3(static_cast<unsigned>(kRow), static_cast<unsigned>((n + kRow - 1) / kRow));
+    return n * threads < (1LL << 32)
+               ? dim3(static_cast<unsigned>(n))
+               : dim3(static_cast<unsigned>(kRow), static_cast<unsigned>((n + kRow - 1) / kRow));
 }
 
 // Outputs of one grouped product, at most (512 GiB of bf16): with P <= 2^31 rows

@@ -144,3 +144,43 @@ def test_int8_experts_of_more_positions_than_one_launch_dimension(moe):
     for i in range(0, T, base):
         n = min(base, T - i)
         assert torch.equal(many[:, i:i + n], few[:, :n]), i
+
+
+@pytest.mark.parametrize("op,T", [("combine", (1 << 26) + 5), ("residual", (1 << 24) + 5)])
+def test_combine_of_more_tokens_than_one_launch_dimension(moe, op, T):
+    """One expert a token, its row the token's own: the combine that ends the
+    whole passes and sums the gradients of a token's pairs.  Every token's row
+    repeats one of 4096."""
+    base, H = 4096, 128
+    print(f"[case] {op} T={T}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(T % 1000)
+    y0 = torch.randn((base, H), generator=gen, device="cuda")
+    w0 = torch.rand((base, 1), generator=gen, device="cuda")
+    gain = torch.rand((H,), generator=gen, device="cuda")
+
+    def run(y, w):
+        n = len(y)
+        p = moe.MoEProblem(n, H, 64, 4, 1, 1, 1, 2.5)
+        rows = torch.arange(n, device="cuda", dtype=torch.int32)
+        if op == "combine":
+            out = torch.full((n, H), float("nan"), dtype=torch.bfloat16, device="cuda")
+            moe.moe_combine(p, y, rows, w, out)
+        else:
+            out = torch.ones((n, H), device="cuda")
+            moe.moe_combine_residual(p, y, rows, w, gain, 1e-6, 3, out)
+        torch.cuda.synchronize()
+        return out
+
+    def many(t):
+        x = torch.empty((T, *t.shape[1:]), device="cuda")
+        x[: T // base * base].view(-1, *t.shape).copy_(t)
+        x[T // base * base:] = t[: T % base]
+        return x
+    few = run(y0, w0)
+    assert not bool(torch.isnan(few).any()) and bool((few != 1).any())
+    out = run(many(y0), many(w0))
+    whole = T // base * base
+    for i in range(0, whole, base * 1024):
+        part = out[i:min(i + base * 1024, whole)].view(-1, base, H)
+        assert bool((part == few).all()), i
+    assert torch.equal(out[whole:], few[: T - whole])
