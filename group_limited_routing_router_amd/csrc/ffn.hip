@@ -282,7 +282,7 @@ hipError_t launch_gemm_nt(const FfnArgs& a, hipStream_t s) {
     const int64_t tiles = mtiles * (a.N / BN_OUT);
     const int64_t grid = (tiles + kNumXcd - 1) / kNumXcd * kNumXcd;
     if (grid <= 0) return hipSuccess;
-    if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+    if (grid > kMaxWorkgroups) return hipErrorInvalidConfiguration;
     ffn_gemm_kernel<BM, BN, WAVES_M, WAVES_N, GATEUP, FP8, SK, NTW>
         <<<dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s>>>(a);
     return hipGetLastError();
@@ -709,7 +709,7 @@ hipError_t launch_gemm_dma(const FfnArgs& a, hipStream_t s) {
     const int64_t tiles = mtiles * (a.N / BN_OUT);
     const int64_t grid = (tiles + kNumXcd - 1) / kNumXcd * kNumXcd;
     if (grid <= 0) return hipSuccess;
-    if (grid > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+    if (grid > kMaxWorkgroups) return hipErrorInvalidConfiguration;
     ffn_gemm_dma_kernel<GATEUP, FP8><<<dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s>>>(a);
     return hipGetLastError();
 }

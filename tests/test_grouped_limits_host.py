@@ -41,3 +41,13 @@ def test_experts_past_the_limit(lib, good):
         assert b"2^38" in lib.moe_last_error()
         assert lib.moe_forward_int8(p, good, good, None, *(good,) * 7, 0, None, None, good, good, n, None) == 2
         assert lib.moe_expert_ffn_backward(p, *(good,) * 11, 0, 0, good, n, None) == 2
+
+
+def test_expert_products_of_more_tiles_than_a_launch(lib, good):
+    """2^31 - 16 positions over 128 columns are more 64-row tiles than one
+    launch takes: refused as such, not launched in part."""
+    p = moe.MoEProblem((TOP - 15) // 16, 128, 64, 16, 1, 1, 16, 1.0)
+    st = lib.moe_expert_gate_up(p, good, good, good, good, good, good, None)
+    assert st == 4 and b"invalid configuration" in lib.moe_last_error()
+    st = lib.moe_expert_down(p, good, good, good, good, None)
+    assert st == 4 and b"invalid configuration" in lib.moe_last_error()
