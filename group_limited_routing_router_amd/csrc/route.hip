@@ -200,7 +200,8 @@ __global__ __launch_bounds__(64 * NW) void route_kernel(
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // uniform per wave
-    const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * tpw;
+    const int64_t tok0 = folded_index() * tpw;
+    if (tok0 >= T) return;
 
     // ---- coalesced load addressing: eight threads per 128-byte row ----
     const uint16_t* wsrc[WL];
@@ -488,7 +489,7 @@ hipError_t launch_route(const Problem& p, const uint16_t* x, const uint16_t* w_r
         // more tokens than one wave of 256 32-token workgroups: 64-token tiles
         // stream the router weight half as often (30% faster at 65536 tokens)
         const int64_t grid = (p.T + 63) / 64;
-        route_kernel<4, 8, 6><<<dim3(static_cast<unsigned>(grid)), dim3(512), 0, s>>>(
+        route_kernel<4, 8, 6><<<folded_grid(grid, 512), dim3(512), 0, s>>>(
             p.T, p.H, p.E, p.G, p.TG, p.k, 64, x, w_router, bias, ids, weights);
     } else if (p.T > 4096) {
         // many tokens: 32-token tiles (the router weight is read once per tile;

@@ -184,3 +184,30 @@ def test_combine_of_more_tokens_than_one_launch_dimension(moe, op, T):
         part = out[i:min(i + base * 1024, whole)].view(-1, base, H)
         assert bool((part == few).all()), i
     assert torch.equal(out[whole:], few[: T - whole])
+
+
+def test_route_of_more_tokens_than_one_launch_dimension(moe):
+    """2^29 + 70 tokens: every one is routed as the same token of a small batch."""
+    base, T, H, E = 16384, (1 << 29) + 70, 128, 4
+    print(f"[case] route T={T}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    x0 = torch.randn((base, H), generator=gen, device="cuda").to(torch.bfloat16)
+    wr = torch.randn((E, H), generator=gen, device="cuda").to(torch.bfloat16)
+    bias = torch.randn((E,), generator=gen, device="cuda")
+
+    def run(x):
+        p = moe.MoEProblem(len(x), H, 64, E, 1, 1, 1, 1.0)
+        ids = torch.full((len(x),), -1, dtype=torch.int32, device="cuda")
+        w = torch.full((len(x),), float("nan"), device="cuda")
+        moe.moe_route(p, x, wr, bias, ids, w)
+        torch.cuda.synchronize()
+        return ids, w
+    few = run(x0)
+    assert len(few[0].unique()) > 1
+    x = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+    whole = T // base * base
+    x[:whole].view(-1, base, H).copy_(x0)
+    x[whole:] = x0[: T - whole]
+    many = run(x)
+    for a, b in zip(many, few):
+        assert bool((a[:whole].view(-1, base) == b).all()) and torch.equal(a[whole:], b[: T - whole])
