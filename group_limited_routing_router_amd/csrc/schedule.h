@@ -8,23 +8,19 @@
 
 #include <stdint.h>
 
-#ifdef __HIP__
-#define MOE_SCHEDULE __host__ __device__ __forceinline__
-#else
-#define MOE_SCHEDULE inline
-#endif
+#include "host_device.h"
 
 namespace moe {
 
 // Row tiles of at most bm rows that n rows take; none for n <= 0.
-MOE_SCHEDULE int row_tiles_of(int n, int bm) {
+MOE_HOST_DEVICE int row_tiles_of(int n, int bm) {
     return n > 0 ? static_cast<int>((static_cast<uint32_t>(n) + (bm - 1)) / bm) : 0;
 }
 
 // Rows of every one of n's tiles but the last: the even share, rounded up to a
 // multiple of gran.  With tiles = row_tiles_of(n, bm) and gran a divisor of bm
 // it is at most bm, so the last tile keeps at least one row.
-MOE_SCHEDULE int rows_per_tile(int n, int tiles, int gran) {
+MOE_HOST_DEVICE int rows_per_tile(int n, int tiles, int gran) {
     const uint32_t share = (static_cast<uint32_t>(n) + (tiles - 1)) / tiles;
     return static_cast<int>((share + (gran - 1)) / gran * gran);
 }

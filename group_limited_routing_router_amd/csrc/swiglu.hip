@@ -6,6 +6,7 @@
 //
 // Both are bound by memory: they read fp32 sums of the products and write
 // codes or bf16 operands of the next ones.
+#include "codes.h"
 #include "common.h"
 #include "kernels.h"
 
@@ -15,7 +16,7 @@ namespace {
 constexpr int kThreads = 256;
 
 // One row a workgroup: h, its largest magnitude, the codes 127 h / amax (to
-// the nearest) and the scale amax / 127.  h stays in registers, CHUNKS groups
+// the nearest, ties to even) and the scale amax / 127.  h stays in registers, CHUNKS groups
 // of 4 a thread; CHUNKS = 0 computes it twice (I > 16384).  Rows of no expert
 // are left out.
 template <int CHUNKS>
@@ -74,14 +75,13 @@ __global__ __launch_bounds__(kThreads) void swiglu_quantize_kernel(const float* 
     // as moe_quantize_rows_int8 treats its rows
     const bool zero = bad || m < 0x1p-100f;
     if (tid == 0) scales[q] = bad ? __builtin_nanf("") : (zero ? 1.0f : m / 127.0f);
-    const float shrink = m > 0x1p100f ? 0x1p-30f : 1.0f, inv = 127.0f / (m * shrink);
+    // large rows are scaled down first, since 127 h would overflow
+    const float shrink = m > 0x1p100f ? 0x1p-30f : 1.0f, ms = m * shrink, inv = 1.0f / ms;
     auto write = [&](int c, const f32x4& v) {
         uint32_t o = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            // |v| <= m, so the code is at most 127 (the quotient may be off by
-            // one rounding of its own)
-            const int code = zero ? 0 : static_cast<int>(fminf(fmaxf(rintf(v[i] * shrink * inv), -127.0f), 127.0f));
+            const int code = zero ? 0 : code_of_f32(v[i] * shrink, ms, inv);
             o |= static_cast<uint32_t>(static_cast<uint8_t>(code)) << (8 * i);
         }
         *reinterpret_cast<uint32_t*>(codes + q * I + c) = o;

@@ -86,7 +86,7 @@ moe_status moe_grouped_gemm_wgrad(const moe_gemm_problem* g, const moe_bf16* dou
 /* Rows of bf16 as 8-bit integers with one fp32 scale each:
  *     amax = max_k |x[r,k]|,  scales[r] = amax / 127,
  *     codes[r,k] = 127 x[r,k] / amax, rounded to the nearest integer (ties to
- *     even; the quotient is the correctly rounded fp32 one)
+ *     even)
  * A row of zeros gets the scale 1 and codes 0; so does a row whose amax is
  * below 2^-100.  A row that holds an infinity or NaN gets the scale NaN and
  * codes 0.
@@ -112,7 +112,7 @@ moe_status moe_grouped_gemm_int8(const moe_gemm_problem* g, const int8_t* a, con
 /* Experts with int8 weights and activations (moe_expert_ffn, moe_forward).
  * The rows of x are quantised as moe_quantize_rows_int8 does it, g and u are
  * int8 products in fp32, h = silu(g) u in fp32 is quantised by rows in the
- * same way (codes to the nearest of the fp32 quotient), y is an int8 product:
+ * same way (127 h / amax to the nearest, ties to even), y is an int8 product:
  *     g[n] = sx s_gate[e,n] (xc . w_gate[e,n]),  u likewise,
  *     y[m] = sh s_down[e,m] (hc . w_down[e,m])
  *   w_gate, w_up  [E,I,H] int8 codes;  s_gate, s_up  [E,I] fp32
