@@ -34,7 +34,9 @@ __global__ __launch_bounds__(kThreads) void swiglu_quantize_kernel(const float* 
         const f32x4 a = *reinterpret_cast<const f32x4*>(gr + c), b = *reinterpret_cast<const f32x4*>(ur + c);
         f32x4 h;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = silu_f32(a[i]) * b[i];
+        // h stays in fp32: the hardware exp2 of silu_f32 is off by 2^-18 at
+        // gates of -80
+        for (int i = 0; i < 4; ++i) h[i] = a[i] * sigmoid_f32(a[i]) * b[i];
         return h;
     };
     float m = 0.0f;

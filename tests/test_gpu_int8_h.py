@@ -54,3 +54,43 @@ def test_ties_of_h(moe, I):
     want = torch.full((I,), 64.0, dtype=torch.float64, device="cuda")
     want[0], want[2::2] = 127, -64
     assert torch.equal(codes, want.expand(T, I))
+
+
+def test_silu_of_far_gates(moe):
+    """Gates from -30 to -84, with up values that bring every h near -1.  h is
+    off by at most six half steps (expf one unit, the sum, the quotient and two
+    products half a unit each): below 2^-21 of itself.  So 127 h / amax is off
+    by at most 127 2^-20, and only a code that close to a half way point may be
+    the next one; the scale and y's own rounding stay within 2^-20."""
+    T, H, I = 512, 128, 128
+    print("[case] far gates", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.zeros((T, H), device="cuda")
+    x[:, 0] = 1
+    x[:, 1:3] = torch.rand((T, 2), generator=gen, device="cuda") * 0.2 - 0.1
+    x = x.to(torch.bfloat16)
+
+    def codes():
+        w = torch.zeros((1, I, H), dtype=torch.int8, device="cuda")
+        w[..., 0] = 127
+        w[..., 1:3] = torch.randint(-1, 2, (1, I, 2), generator=gen, device="cuda")
+        return w
+    w_gate, w_up = codes(), codes()
+    far = torch.linspace(30, 84, I, dtype=torch.float64, device="cuda")[None]
+    s_gate = (-far / 127).float()
+    s_up = (torch.exp(far) / far / 127).float()
+    y = expert(moe, x, w_gate, s_gate, w_up, s_up, I).double()
+    xc = torch.empty((T, H), dtype=torch.int8, device="cuda")
+    xs = torch.empty((T,), device="cuda")
+    moe.moe_quantize_rows_int8(x, xc, xs)
+    a, s = xc.double(), xs[:, None]
+    g = ((a @ w_gate[0].double().T).float() * (s * s_gate)).double()
+    u = ((a @ w_up[0].double().T).float() * (s * s_up)).double()
+    assert float(g.max()) < -29 and float(g.min()) < -83
+    h = g / (1 + torch.exp(-g)) * u
+    amax = h.abs().amax(dim=1, keepdim=True)
+    v = 127 * h / amax
+    near = ((v - torch.floor(v) - 0.5).abs() < 127 * 2.0 ** -20).double()
+    step = amax / 127
+    err = (y - torch.round(v) * step).abs() - 2.0 ** -20 * torch.round(v).abs() * step
+    assert bool((err <= near * step).all()), float((err / step).max())
