@@ -36,13 +36,15 @@ __device__ __forceinline__ int64_t source_row(const GemmArgs& g, int64_t q) {
     return r < 0 ? 0 : (r >= g.S ? g.S - 1 : r);
 }
 
-// The plain kernel: one 64 x 64 tile of the output, the reduction in steps of
-// 64 bytes a row through LDS.  In LDS both operands lie with the reduction
+// The plain kernel, for rows gathered from more than 4 GiB (the tiles address
+// them with 32-bit offsets): one 64 x 64 tile of the product or the weight
+// gradient, the reduction in steps of 64 bytes a row through LDS.  In LDS both operands lie with the reduction
 // along the row; an operand whose reduction runs down the rows in memory is
 // transposed on the way in.  Grid: (column tiles, row tiles of the fullest
 // possible expert or, for the weight gradient, row tiles of N, experts).
 template <int MODE, bool I8>
 __global__ __launch_bounds__(kThreads) void gemm_plain_kernel(GemmArgs g) {
+    static_assert(MODE != kInputGrad, "gathers nothing");
     constexpr int EB = I8 ? 1 : 2;        // bytes per operand element
     constexpr int PER16 = 16 / EB;        // elements per 16 bytes
     constexpr int BK = 64 / EB;           // reduction per step
@@ -56,7 +58,7 @@ __global__ __launch_bounds__(kThreads) void gemm_plain_kernel(GemmArgs g) {
     // output: rows [r0, rows) x columns [c0, cols); reduction over [0, red)
     const int64_t rows = MODE == kWeightGrad ? g.N : n_e;
     const int cols = MODE == kProduct ? g.N : g.K;
-    const int64_t red = MODE == kProduct ? g.K : (MODE == kInputGrad ? g.N : n_e);
+    const int64_t red = MODE == kProduct ? g.K : n_e;
     const int c0 = blockIdx.x * 64;
     const unsigned char* a = static_cast<const unsigned char*>(g.a);
     const unsigned char* w = static_cast<const unsigned char*>(g.w) +
@@ -87,9 +89,7 @@ __global__ __launch_bounds__(kThreads) void gemm_plain_kernel(GemmArgs g) {
                     const int rr = tid >> 2, kk = (tid & 3) * PER16;
                     if (r0 + rr < rows && k0 + kk < red) {
                         const int64_t q = first + r0 + rr;
-                        v = MODE == kProduct
-                                ? ld16(a + (source_row(g, q) * g.K + k0 + kk) * EB)
-                                : ld16(static_cast<const unsigned char*>(g.dout) + (q * g.N + k0 + kk) * EB);
+                        v = ld16(a + (source_row(g, q) * g.K + k0 + kk) * EB);
                     }
                     *reinterpret_cast<u32x4*>(&s_y[rr * PITCH + (tid & 3) * 16]) = v;
                 }
@@ -104,9 +104,7 @@ __global__ __launch_bounds__(kThreads) void gemm_plain_kernel(GemmArgs g) {
                 } else {
                     const int kk = tid >> 3, cc = (tid & 7) * 8;
                     if (k0 + kk < red && c0 + cc < cols)
-                        v = MODE == kInputGrad
-                                ? ld16(w + ((k0 + kk) * g.K + c0 + cc) * EB)
-                                : ld16(a + (source_row(g, first + k0 + kk) * g.K + c0 + cc) * EB);
+                        v = ld16(a + (source_row(g, first + k0 + kk) * g.K + c0 + cc) * EB);
                     const uint16_t* h = reinterpret_cast<const uint16_t*>(&v);
                     for (int i = 0; i < 8; ++i)
                         *reinterpret_cast<uint16_t*>(&s_x[(cc + i) * PITCH + kk * 2]) = h[i];
@@ -328,7 +326,9 @@ __global__ __launch_bounds__(kThreads) void join_splits_kernel(GemmArgs g, int s
 
 template <int MODE, bool I8>
 hipError_t launch(const GemmArgs& g, hipStream_t s) {
-    if (!gather_fits(g, I8 ? 1 : 2)) return launch_plain<MODE, I8>(g, s);
+    // the input gradient gathers nothing, whatever pairs its caller has
+    if constexpr (MODE == kProduct)
+        if (!gather_fits(g, I8 ? 1 : 2)) return launch_plain<MODE, I8>(g, s);
     const TilePlan p = plan_tiles<MODE, I8>(g);
     hipError_t err;
     if (p.rows == 256)

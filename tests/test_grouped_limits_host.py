@@ -51,3 +51,13 @@ def test_expert_products_of_more_tiles_than_a_launch(lib, good):
     assert st == 4 and b"invalid configuration" in lib.moe_last_error()
     st = lib.moe_expert_down(p, good, good, good, good, None)
     assert st == 4 and b"invalid configuration" in lib.moe_last_error()
+
+
+def test_the_input_gradient_has_one_kernel():
+    """The kernel for rows gathered from more than 4 GiB exists for the
+    products that gather (product, int8 product, weight gradient) and for them
+    alone: the input gradient runs on the tiles at every size."""
+    with open(moe.library_path(), "rb") as f:
+        lib = f.read()
+    assert [f"gemm_plain_kernelILi{mode}ELb{i8}E".encode() in lib
+            for mode, i8 in ((0, 0), (0, 1), (2, 0), (1, 0))] == [True, True, True, False]
