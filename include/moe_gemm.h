@@ -20,6 +20,11 @@
  * E = 1, expert_offsets may be NULL: the one group then takes all P rows (a
  * dense layer).
  *
+ * Rows gathered by sorted_pairs from an activation tensor of more than 4 GiB
+ * less 1 MiB (S K 2 bytes, S K for int8) run on a simpler kernel: the product
+ * about 3.5 times and the weight gradient 6.5 times slower (420000 rows of 5120
+ * to 2560 columns: 31 and 83 ms against 9 and 13).
+ *
  * A row that holds an infinity or NaN affects its own output row alone (in
  * the weight gradient, its own expert's gradient).
  */
