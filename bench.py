@@ -56,12 +56,14 @@ if ROOT not in sys.path:
 PEAK_BF16 = 2.5166e15   # dense bf16 MFMA, FLOP/s (MI355X published)
 PEAK_HBM = 8.0e12       # HBM3E, B/s (MI355X published)
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "traffic.json")
-# the sources of the MoE block's kernels (the measurement kernels of peak.hip
-# are not part of the block and do not invalidate its stored traffic)
+# the sources of the MoE block's kernels (the measurement kernels of peak.hip,
+# the products by themselves and what runs on them are not part of the block's
+# forward pass and do not invalidate its stored traffic)
+OTHER_SOURCES = {"peak.hip", "grouped.hip", "gemm_tile.h", "gemm_wgrad.h", "swiglu.hip", "codes.h"}
 KERNEL_SOURCES = sorted(
     os.path.join("group_limited_routing_router_amd", "csrc", f)
     for f in os.listdir(os.path.join(ROOT, "group_limited_routing_router_amd", "csrc"))
-    if f.endswith((".hip", ".h")) and f != "peak.hip")
+    if f.endswith((".hip", ".h")) and f not in OTHER_SOURCES)
 STEPS = ["route", "permute", "gate_up", "down", "combine", "combine_residual"]
 
 
