@@ -76,8 +76,8 @@ moe_status check_problem(const moe_problem* p) {
     if (p->k < 1 || p->k > cand)
         return fail(MOE_ERR_INVALID_ARG, "k=%d must be in [1, TG*E/G=%lld]", p->k, (long long)cand);
     if (!isfinite(p->scale)) return fail(MOE_ERR_INVALID_ARG, "scale is not finite");
-    if (p->T * static_cast<int64_t>(p->k) > 0x7fffffffLL)
-        return fail(MOE_ERR_INVALID_ARG, "T*k=%lld exceeds int32", (long long)(p->T * p->k));
+    if (p->T > 0x7fffffffLL / p->k)  // T * k itself may pass 64 bits
+        return fail(MOE_ERR_INVALID_ARG, "T=%lld times k=%d exceeds int32", (long long)p->T, p->k);
     if (p->E > 256) return fail(MOE_ERR_UNSUPPORTED, "E=%d > 256", p->E);
     if (p->k > 16) return fail(MOE_ERR_UNSUPPORTED, "k=%d > 16", p->k);
     if (p->H % 128 != 0) return fail(MOE_ERR_UNSUPPORTED, "H=%d is not a multiple of 128", p->H);

@@ -4,7 +4,8 @@
  * and in 8-bit integers with a scale for each token and each output channel.
  *
  * The conventions of moe.h hold: device pointers owned by the caller,
- * contiguous, row-major, 16-byte aligned; nothing is allocated, freed or
+ * contiguous, row-major, 16-byte aligned, no output overlapping an input or
+ * another output; nothing is allocated, freed or
  * synchronised; every argument is checked on the host before anything is
  * enqueued; no memset, so every call can be captured into a HIP graph; no
  * atomics, so results are the same from run to run.

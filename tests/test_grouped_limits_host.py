@@ -61,3 +61,13 @@ def test_the_input_gradient_has_one_kernel():
         lib = f.read()
     assert [f"gemm_plain_kernelILi{mode}ELb{i8}E".encode() in lib
             for mode, i8 in ((0, 0), (0, 1), (2, 0), (1, 0))] == [True, True, True, False]
+
+
+def test_tokens_times_experts_past_64_bits(lib, good):
+    """T k that wraps to a small number is refused like any other past int32."""
+    for T, k in ((1 << 62, 4), ((1 << 62) + 3, 4), (1 << 61, 8), (1 << 31, 1), ((1 << 30) + 1, 2)):
+        p = moe.MoEProblem(T, 128, 64, 16, 1, 1, k, 1.0)
+        assert moe.moe_workspace_bytes(p) == 0, (T, k)
+        assert moe.moe_int8_workspace_bytes(p) == 0 and moe.moe_backward_workspace_bytes(p) == 0
+        assert lib.moe_expert_ffn_int8(p, *(good,) * 10, good, 1 << 50, None) == 1
+        assert b"int32" in lib.moe_last_error()
