@@ -26,6 +26,7 @@
 //    lanes, lane i reads 4 elements of row i / 4 and receives column i of
 //    the 4 x 16 block).  The swizzle puts the 4 rows x 64 bytes that 32 lanes
 //    read on all 64 banks once.
+// Measured with the epilogue: 0-6% of the LDS cycles lost to bank conflicts.
 // X is loaded two stages ahead into three buffers, Y one ahead into two; the
 // 32-row tile (few rows, where the weight stream is all the time there is)
 // loads both three stages ahead into four.

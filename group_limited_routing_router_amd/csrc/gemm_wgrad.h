@@ -23,6 +23,11 @@
 // after a tile therefore allow for its stores (exactly as many as the store
 // instructions, which are issued for every lane; lanes outside the output
 // get an offset past its end, which drops them).
+//
+// 8192 tokens, 256 experts of 2560 x 5120, bf16: 2.65 ms, 9.0 GB moved (6.7 of
+// them the output), the matrix units busy 31% of it, a fifth of the LDS cycles
+// lost to bank conflicts.  With accumulate a tile's values are read one load
+// at a time, each waited for: 128 tokens, 2.4 ms written and 9.9 ms added to.
 #pragma once
 
 #include "gemm_tile.h"

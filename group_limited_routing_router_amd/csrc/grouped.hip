@@ -263,7 +263,12 @@ TilePlan plan_tiles(const GemmArgs& g) {
             // rows, K 2232: 112 us on 128 rows, 76 on 256)
             const float lines = g.K * eb % 128 == 0 ? 1.0f : (rows == 256 ? 1.1f : 1.3f);
             float t = tile_time(rows, tiles_of(rows) * splits, lines * stages / splits);
-            // the sums written and read, and one more launch
+            // the sums written and read, one more launch, and 5% for the parts'
+            // own first loads.  Of 1, 2, 4, 8, 16 parts: 32 rows, 512 x 16384:
+            // 58, 36, 24, 19, 19 us, 16 taken; 256 rows, 2048 x 4096: 21, 22,
+            // 20, 22, 26, 1 taken; 8192 rows, 5120 x 20480: 1367, 1350, 1446,
+            // 1708, 2249, 1 taken; worst of twelve shapes: 8 x 128 rows, 1024 x
+            // 4096: 22, 30, 28, 31, 43, 2 taken
             if (splits > 1) t = 1.05f * t + 4.0f + 2.0f * splits * static_cast<float>(g.P) * cols * 4.0f / 5e6f;
             if (best < 0.0f || t < best) {
                 best = t;
@@ -355,8 +360,11 @@ struct WgradPlan {
 
 WgradPlan plan_wgrad(const GemmArgs& g) {
     // 256 x 256 tiles from about two for each compute unit on (256 experts of
-    // 2560 x 5120, 256 rows each: 2.6 against 3.5 ms; 24 experts of 776 x
-    // 1000 make 384 of them: 43 us on 1344 smaller ones)
+    // 2560 x 5120, 256 rows each: 2.6 against 3.5 ms).  Large against small
+    // tiles at 256 rows an expert: 320 of them (one expert of 4096 x 5120) 26.0
+    // and 21.5 us, 384 (24 of 776 x 1000) 27.9 and 26.1, 512 (32 of these) 29.2
+    // and 29.1, 512 (32 of 1024 x 1024) 29.6 and 31.5, 1024 (64 of 776 x 1000)
+    // 50.0 and 52.9
     WgradPlan p{static_cast<int64_t>((g.K + 255) / 256) * ((g.N + 255) / 256) * g.E >= 512, 1};
     if (p.big) return p;
     // Parts of the positions, where the sums are long.  Microseconds: a stage
@@ -431,7 +439,7 @@ __device__ __forceinline__ int code_of(float x, float m, float inv) {
 // Rows of bf16 as 8-bit codes with one scale each, LANES lanes a row.  A row
 // is read once and stays in registers (CHUNKS 16-byte pieces a lane); CHUNKS =
 // 0 reads it twice (K > 16384).  Bound by memory: 8192 rows of 5120 (126 MB
-// read and written).
+// read and written) 32-35 us, 3.6-3.9 TB/s.
 template <int LANES, int CHUNKS>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const uint16_t* x, int64_t rows, int K,
                                                                  int8_t* codes, float* scales) {
@@ -544,7 +552,10 @@ hipError_t launch_quantize_rows(int64_t rows, int K, const uint16_t* x, int8_t* 
                                 hipStream_t s) {
     if (rows <= 0) return hipSuccess;
     const dim3 threads(kThreads), whole = folded_grid(rows), waves = folded_grid((rows + 3) / 4);
-    if (rows < 2048 && K > 512 && K <= 2048)  // few rows: a workgroup each (301 rows of 2000: 3.4 against 5.5 us)
+    // few rows: a workgroup each rather than a wave (rows of 1040: 301 3.0
+    // against 5.2 us, 2048 4.6 and 5.5, 4096 6.7 and 7.3, 8192 11.5 and 10.9,
+    // 32768 36.7 and 29.5)
+    if (rows < 2048 && K > 512 && K <= 2048)
         quantize_rows_kernel<kThreads, 1><<<whole, threads, 0, s>>>(x, rows, K, codes, scales);
     else if (K <= 512)
         quantize_rows_kernel<kWave, 1><<<waves, threads, 0, s>>>(x, rows, K, codes, scales);
