@@ -25,8 +25,8 @@ offsets[e + 1], position q belongs to token sorted_pairs[q] // k.
                 form leaves mean out and takes the mean square for var
     norm_grad   from dy: dx and the gradients of weight and bias
 
-Activations, gradients and FFN outputs are bf16, the residual stream that the
-norm reads fp32 or bf16.
+Activations, gradients and the outputs of products are bf16 (beside operands of
+4 significant bits), the residual stream that the norm reads fp32 or bf16.
 """
 import math
 
@@ -44,13 +44,13 @@ def listed():
     block = dict(E=EXPERTS, k=TOP, skew=0.0)
     return [
         # a decode batch: 4 rows for each expert, every weight read once
-        dict(name="product decode", op="product", T=128, N=INTER, K=HIDDEN, out="bf16", **block),
+        dict(name="product decode", op="product", T=128, N=INTER, K=HIDDEN, **block),
         # a prefill chunk: 256 rows for each expert
-        dict(name="product prefill", op="product", T=8192, N=INTER, K=HIDDEN, out="bf16", **block),
+        dict(name="product prefill", op="product", T=8192, N=INTER, K=HIDDEN, **block),
         # the gradient of the down projection's input, busy and idle experts
-        dict(name="input_grad skewed", op="input_grad", T=4096, k=TOP, E=EXPERTS, N=HIDDEN, K=INTER, out="bf16", skew=0.7),
+        dict(name="input_grad skewed", op="input_grad", T=4096, k=TOP, E=EXPERTS, N=HIDDEN, K=INTER, skew=0.7),
         # few experts, sizes that end inside a block, rows in sorted order
-        dict(name="input_grad odd", op="input_grad", T=5003, k=1, E=24, N=1008, K=784, out="f32", skew=0.5),
+        dict(name="input_grad odd", op="input_grad", T=5003, k=1, E=24, N=1008, K=784, skew=0.5),
         # a dense layer for one token: a launch's latency and the weights once
         dict(name="ffn one token", op="ffn", T=1, k=1, E=1, H=HIDDEN, I=20480, skew=0.0),
         # the experts of a prefill chunk
@@ -97,7 +97,7 @@ def draw(rng):
         N, K = max(64, N // 2 // 16 * 16), max(64, K // 2 // 16 * 16)
     while T * k * N * K > 8192 * TOP * INTER * HIDDEN:
         T = max(1, T // 2)
-    return dict(op=op, T=T, k=k, E=E, N=N, K=K, out=rng.choice(["f32", "bf16"]), skew=skew)
+    return dict(op=op, T=T, k=k, E=E, N=N, K=K, skew=skew)
 
 
 # ---- quantisation, for the inputs and the plain form ----
@@ -109,6 +109,11 @@ def _exponents(amax):
     return torch.where(amax > 0, e - 9 + (m > 0.875).to(e.dtype), torch.zeros_like(e))
 
 
+def _power(e):
+    """2^e, exactly, for -127 < e < 128."""
+    return ((e.int() + 127) << 23).view(torch.float32)
+
+
 def _fp8(x):
     """fp32 values of at most 448 rounded to e4m3."""
     return x.to(torch.float8_e4m3fn)
@@ -117,14 +122,14 @@ def _fp8(x):
 def _padded(x):
     """x [R, C] with C filled up to whole blocks, as [R, blocks, 128]."""
     x = torch.nn.functional.pad(x, (0, -x.shape[1] % BLOCK))
-    return x.reshape(x.shape[0], -1, BLOCK)
+    return x.reshape(x.shape[0], x.shape[1] // BLOCK, BLOCK)
 
 
 def _rounded_rows(x):
     """The rows of x quantised by blocks and dequantised, in fp32."""
     p = _padded(x)
     e = _exponents(p.abs().amax(dim=2, keepdim=True))
-    return torch.ldexp(_fp8(torch.ldexp(p, -e)).float(), e).reshape(x.shape[0], -1)[:, : x.shape[1]]
+    return (_fp8(p * _power(-e)).float() * _power(e)).reshape(p.shape[0], p.shape[1] * BLOCK)[:, : x.shape[1]]
 
 
 def _spread(s, rows, cols):
@@ -135,7 +140,7 @@ def _spread(s, rows, cols):
 def _weights(s, name, e):
     """Weight matrix e of a stack, dequantised, in fp32."""
     w, scales = s["q_" + name][e], s["s_" + name][e]
-    return torch.ldexp(w.float(), _spread(scales.int() - 127, *w.shape))
+    return w.float() * _spread(_power(scales.int() - 127), *w.shape)
 
 
 # ---- inputs ----
@@ -150,7 +155,7 @@ def _stack(E, N, K, gen):
         p = torch.nn.functional.pad(w, (0, -K % BLOCK, 0, -N % BLOCK))
         p = p.reshape(scales.shape[1], BLOCK, scales.shape[2], BLOCK)
         e = _exponents(p.abs().amax(dim=(1, 3)))
-        codes[i] = _fp8(torch.ldexp(w, -_spread(e, N, K)))
+        codes[i] = _fp8(w * _spread(_power(-e), N, K))
         scales[i] = (e + 127).to(torch.uint8)
     return codes, scales
 
@@ -220,7 +225,7 @@ def prepare(case, seed):
         s["pairs"] = s["tokens"] = None  # rows already in sorted order
     s["a" if op == "product" else "dout"] = _acts((T, K), gen) if op == "product" else _grads((P, N), gen)
     s["q_w"], s["s_w"] = _stack(E, N, K, gen)
-    s["out"] = torch.empty((P, N if op == "product" else K), dtype=torch.float32 if case["out"] == "f32" else torch.bfloat16, device="cuda")
+    s["out"] = torch.empty((P, N if op == "product" else K), dtype=torch.bfloat16, device="cuda")
     return s
 
 
@@ -364,9 +369,9 @@ def work(case):
         if case["op"] == "ffn":
             return {"bytes": 2 * T * H + 3 * met * H * I + 2 * P * H + index, "flops": 6.0 * P * H * I}
         return {"bytes": 2 * T * H + 2 * P * H + 3 * met * H * I + 2 * P * H + 6 * E * H * I + index, "flops": 16.0 * P * H * I}
-    N, K, out = case["N"], case["K"], 4 if case["out"] == "f32" else 2
+    N, K = case["N"], case["K"]
     read, written = (T * K, P * N) if case["op"] == "product" else (P * N, P * K)
-    return {"bytes": 2 * read + met * N * K + out * written + index, "flops": 2.0 * P * N * K}
+    return {"bytes": 2 * read + met * N * K + 2 * written + index, "flops": 2.0 * P * N * K}
 
 
 # ---- the definition in 64 bits ----
