@@ -14,6 +14,12 @@ _BINDING_NAMES = (
     "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad", "moe_quantize_rows_int8",
     "moe_grouped_gemm_int8", "moe_int8_workspace_bytes", "moe_expert_ffn_int8",
     "moe_forward_int8", "moe_backward_workspace_bytes", "moe_expert_ffn_backward",
+    "moe_fp8_block_scales", "moe_quantize_rows_fp8_block", "moe_quantize_weights_fp8_block",
+    "moe_grouped_gemm_fp8_block", "moe_grouped_gemm_fp8_block_dgrad",
+    "moe_expert_gate_up_fp8_block", "moe_fp8_block_workspace_bytes", "moe_expert_ffn_fp8_block",
+    "moe_forward_fp8_block", "moe_fp8_block_backward_workspace_bytes",
+    "moe_expert_ffn_fp8_block_backward", "moe_norm", "moe_norm_workspace_bytes",
+    "moe_norm_backward",
     "MoEGemmProblem",
     "moe_workspace_bytes", "MoEProblem", "MoEError", "DTYPE_F32", "DTYPE_BF16",
     "load_library", "library_path",

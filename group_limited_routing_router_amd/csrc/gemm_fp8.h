@@ -1,0 +1,625 @@
+// gemm_fp8.h -- the tiled kernel of the FP8 products with a scale for each
+// block of 128 (moe_fp8.h).
+//
+//   out[q,c] = sum over blocks b of 2^(sy[row(q),b] + sx[e,b,c / 128])
+//              sum over r in b of y[row(q),r] x[e,r,c]
+//
+// on e4m3 codes.  Scales are powers of two, so the scaled matrix instruction
+// (32x32x64, twice the rate of bf16) applies them to its sums by itself and
+// the fp32 accumulators never leave the matrix registers: with fp32 scales
+// every block of the reduction would end in 16 multiply-adds a lane for each
+// 32 x 32 of output, on registers that the vector unit can reach.
+//
+// The tile and its LDS layout are those of gemm_tile.h: 4 waves, BY rows of an
+// expert by BX columns, operands loaded straight into LDS in stages of 128
+// bytes a row.  A stage is one block of the reduction, two matrix
+// instructions deep, so a lane needs one scale byte for each of its rows and
+// one for its columns a stage.  The rows' scales are read 40 stages at a time
+// into registers (LDS is full) and shifted down; the columns' lie one stage
+// to a lane and are broadcast.
+//
+// Sums.  Measured: the matrix instructions add groups of 8 products, each cut
+// towards zero to a multiple of 2^-13 of the largest's power of two, and sum
+// the groups in fp32.  On normal values the cut is 1.5e-5 of the result, on
+// equal signs 8e-5: 200 times below the operands' own rounding (2^-4), and
+// below that of a bf16 output (2^-8).  Products widened to bf16 would be summed in
+// fp32 throughout, at half the rate.
+//
+// Three forms:
+//   kF8Product    x = w[e] rows along K
+//   kF8InputGrad  x = w[e] columns: the stage holds 128 rows of BX codes and
+//                 the operand is read with the transposing LDS load
+//                 (ds_read_b64_tr_b8: in each group of 16 lanes, lane i reads
+//                 8 codes of row i / 2 and receives column i of the 8 x 16
+//                 block).  Chunk c of row r lies at place c ^ down_swizzle(r),
+//                 so that the 8 rows x 32 bytes of 32 lanes lie on all banks
+//                 once.  A second matrix may follow the first in the reduction
+//                 (dx = dg . gate + du . up in one pass).
+//   kF8GateUp     BX / 2 columns of gate and the same of up, in turn by wave,
+//                 so that a lane ends with g and u of the same places; BX / 2
+//                 = 128 is a block of h, whose scale needs only its own tile.
+#pragma once
+
+#include "fp8_codes.h"
+#include "fp8_kernels.h"
+#include "gemm_tile.h"
+#include "tile_plan.h"
+
+namespace moe {
+namespace {
+
+enum Fp8Mode { kF8Product = 0, kF8InputGrad = 1, kF8GateUp = 2, kF8GateUpGrad = 3 };
+
+// A pointer that is the same in every lane, in scalar registers.
+__device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+    return reinterpret_cast<const uint8_t*>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+typedef int32_t i32x2 __attribute__((ext_vector_type(2)));
+
+// One 32x32x64 step on e4m3 codes: lane l supplies 32 codes of row (or column)
+// l % 32, half l / 32 of the 64; any order within the 64, the same for both.
+// sa, sb: scale bytes in the low 8 bits.
+__device__ __forceinline__ f32x16 mfma32_fp8(const i32x8& a, const i32x8& b, const f32x16& c, int sa, int sb) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, sa, 0, sb);
+}
+
+__device__ __forceinline__ u32x2 lds_read_tr8(const unsigned char* p) {
+    return __builtin_bit_cast(
+        u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                   (__attribute__((address_space(3))) i32x2*)const_cast<unsigned char*>(p)));
+}
+
+// Rows of 256 bytes: 8 of them put 32 bytes on each eighth of the banks; rows
+// of 128: the parity of the row is one bit of the bank already.
+template <int BX>
+__device__ __forceinline__ int down_swizzle(int r) {
+    return BX >= 256 ? (r & 7) << 1 : ((r >> 1) & 3) << 1;
+}
+
+// Four fp32 -> four e4m3 codes (nearest even), the first in the low byte.
+__device__ __forceinline__ uint32_t pack_fp8(float a, float b, float c, float d) {
+    int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true));
+}
+
+// Codes of four values in a block whose largest magnitude has the bits top.
+__device__ __forceinline__ uint32_t block_codes(const f32x4& v, uint32_t top, float inverse) {
+    if (top >= kInfBits) return 0x7f7f7f7fu;
+    if (top < kTinyBits) return 0;
+    return pack_fp8(v[0] * inverse, v[1] * inverse, v[2] * inverse, v[3] * inverse);
+}
+
+__device__ __forceinline__ uint32_t magnitude_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// Words of a row's scales held in registers: 40 stages, K = 5120.
+constexpr int kScaleWords = 10;
+
+template <int MODE, int BX, int BY, bool GATHER, bool NT>
+__global__ __launch_bounds__(kThreads, (TileShape<BX, BY>::kPerCu)) void fp8_tile_kernel(Fp8Args g) {
+    typedef TileShape<BX, BY> Shape;
+    constexpr bool TRX = MODE == kF8InputGrad;
+    constexpr bool GATED = MODE == kF8GateUp || MODE == kF8GateUpGrad;
+    constexpr int PARTS = MODE == kF8Product ? 1 : 2;    // weight matrices
+    constexpr int WY = Shape::kWavesY, WX = Shape::kWavesX;
+    constexpr int XB = BX / 32 / WX, YB = BY / 32 / WY;  // 32-blocks per wave
+    constexpr int COLS = GATED ? BX / 2 : BX;            // output columns of the tile
+    constexpr int WCOLS = COLS / WX;                     // and of a wave
+    static_assert(WCOLS <= kBlock && kBlock % WCOLS == 0, "a wave's columns lie in one block");
+    static_assert(!GATED || (COLS == kBlock && XB % 2 == 0), "a tile is a block of h");
+    constexpr int XS = Shape::kXStage, YS = Shape::kYStage;
+    constexpr int XBUFS = Shape::kXBufs, YBUFS = Shape::kYBufs;
+    constexpr int XA = XBUFS - 1, YA = YBUFS - 1;        // stages the loads run ahead
+    constexpr int DMA_X = BX / 32, DMA_Y = BY / 32;      // 1 KB loads per wave and stage
+    // loads younger than those of the next stage, at a stage's end: each stage
+    // loads Y first, then X
+    constexpr int YOUNGER = YA == 1 ? DMA_X : (XA - 1) * (DMA_X + DMA_Y);
+    static_assert(YA == 1 ? XA >= 1 : XA == YA, "the count above");
+
+    __shared__ __attribute__((aligned(1024))) unsigned char s_arena[Shape::kArena];
+    const uint32_t arena = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(s_arena));
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int cols = MODE == kF8InputGrad ? g.K : g.N;
+    const int col_tiles = (cols + COLS - 1) / COLS;
+
+    int e, nt, row0, rows;
+    {
+        int32_t* s_off = reinterpret_cast<int32_t*>(s_arena);
+        int32_t* s_tstart = s_off + (kMaxE + 1);
+        if (!find_tile<BY, BY >= 64 ? 64 : 1, kBand>(g.offsets, g.P, g.E, col_tiles, s_off, s_tstart, e, nt, row0, rows)) return;
+        e = __builtin_amdgcn_readfirstlane(e);
+        nt = __builtin_amdgcn_readfirstlane(nt);
+        row0 = __builtin_amdgcn_readfirstlane(row0);
+        rows = __builtin_amdgcn_readfirstlane(rows);
+        __syncthreads();  // everyone is done with the schedule before the arena is reused
+    }
+    const int c0 = nt * COLS;
+    const int64_t orow0 = row0;
+    const int nblk = (rows + 31) >> 5;
+    const int64_t K = g.K, N = g.N;
+    const int NB = (g.N + kBlock - 1) / kBlock, KB = (g.K + kBlock - 1) / kBlock;
+    // stages: blocks of the reduction; input grad: those of both matrices
+    const int part_stages = TRX ? NB : KB;
+    const int nk = TRX && g.w[1] ? 2 * NB : part_stages;
+    const int s0 = static_cast<int>(static_cast<int64_t>(nk) * blockIdx.y / gridDim.y);
+    const int s1 = static_cast<int>(static_cast<int64_t>(nk) * (blockIdx.y + 1) / gridDim.y);
+    const bool split = gridDim.y > 1;
+
+    // ---- loads (gemm_tile.h) ----
+    const int64_t matrix = static_cast<int64_t>(e) * N * K + static_cast<int64_t>(c0) * (TRX ? 1 : K);
+    const uint8_t* xbase[PARTS];
+    const uint8_t* xscale[PARTS];
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) {
+        xbase[p] = g.w[p] + matrix;
+        xscale[p] = g.w_scale[p] + static_cast<int64_t>(e) * NB * KB;
+    }
+    const uint8_t* ybase = g.y + (GATHER ? 0 : orow0 * g.y_cols);
+    uint32_t vx[DMA_X], vy[DMA_Y];
+    auto along_row = [&](int j, int per_wave) { return wave * per_wave + j * 8 + (lane >> 3); };
+    auto along_chunk = [&](int r) { return (lane & 7) ^ ((r >> 1) & 7); };
+    auto gather_row = [&](int r) -> int64_t {  // the row of y of output row r
+        const int64_t q = orow0 + min(r, rows - 1);
+        if constexpr (!GATHER) return q;
+        const int64_t s = g.pairs[q] / g.k;
+        return s < 0 ? 0 : (s >= g.S ? g.S - 1 : s);
+    };
+    // gated: the matrix and column of a stage's row, wave by wave: gate, up
+    constexpr int HALF = BX / WX / 2;
+    auto x_part = [&](int j) { return GATED ? (wave * (BX / 4) + j * 8) / HALF % 2 : 0; };
+#pragma unroll
+    for (int j = 0; j < DMA_X; ++j) {
+        if constexpr (TRX) {
+            const int r = wave * 32 + j * (1024 / BX) + lane / (BX / 16);
+            const int c = (lane % (BX / 16)) ^ down_swizzle<BX>(r);
+            vx[j] = static_cast<uint32_t>(r * K + c * 16);
+        } else {
+            const int r = along_row(j, BX / 4);
+            const int col = GATED ? r / (2 * HALF) * HALF + r % HALF : r;
+            vx[j] = static_cast<uint32_t>(col * K + along_chunk(r) * 16);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < DMA_Y; ++j) {
+        const int r = along_row(j, BY / 4);
+        const int c = along_chunk(r);
+        if (r >= nblk * 32)
+            vy[j] = kNoRowOffset;
+        else if constexpr (GATHER)
+            vy[j] = static_cast<uint32_t>(gather_row(r) * g.y_cols + c * 16);
+        else
+            vy[j] = static_cast<uint32_t>(r * g.y_cols + c * 16);
+    }
+    // chunks of a matrix's last stage that lie inside the reduction (along
+    // rows; the rows of y of two matrices are padded to whole blocks)
+    const int tail = (TRX ? (g.w[1] ? kBlock : g.N - (NB - 1) * kBlock) : g.K - (KB - 1) * kBlock) / 16;
+    auto x_buf = [&](int i) { return arena + i * XS; };
+    auto y_buf = [&](int i) { return arena + XBUFS * XS + i * YS; };
+    const __amdgpu_buffer_rsrc_t rsrc_y =
+        make_rsrc(uniform(ybase), __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
+                                      (GATHER ? g.S : static_cast<int64_t>(rows)) * g.y_cols)));
+    auto dma_x = [&](int j, int buf, int kt) {
+        const uint32_t at = x_buf(buf) + wave * (XS / 4) + j * 1024;
+        if constexpr (TRX) {
+            // the buffer starts at the stage's first row and ends with its
+            // last row inside the reduction
+            const bool second = kt >= part_stages;
+            const int kk = second ? kt - part_stages : kt;
+            const int valid = min(kBlock, g.N - kk * kBlock);
+            dma_load16<NT>(at,
+                           make_rsrc(uniform((second ? xbase[1] : xbase[0]) + static_cast<int64_t>(kk) * kBlock * K),
+                                     __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(valid * K - c0))),
+                           vx[j], 0);
+        } else {
+            const bool past = kt == nk - 1 && along_chunk(along_row(j, BX / 4)) >= tail;
+            const uint32_t bytes = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(min(COLS, cols - c0) * K));
+            const uint8_t* base = GATED && x_part(j) ? xbase[PARTS - 1] : xbase[0];
+            dma_load16<NT>(at, make_rsrc(uniform(base), bytes), past ? kNoRowOffset : vx[j], static_cast<uint32_t>(kt * 128));
+        }
+    };
+    auto dma_y = [&](int j, int buf, int kt) {
+        const uint32_t at = y_buf(buf) + wave * (YS / 4) + j * 1024;
+        const bool past = kt == nk - 1 && along_chunk(along_row(j, BY / 4)) >= tail;
+        dma_load16(at, rsrc_y, past ? kNoRowOffset : vy[j], static_cast<uint32_t>(kt * 128));
+    };
+
+    const int wy = wave / WX, wx = wave % WX;
+    const int r32 = lane & 31, half = lane >> 5;
+    int valid_blocks = 0;
+#pragma unroll
+    for (int m = 0; m < YB; ++m) valid_blocks += (wy + WY * m) < nblk;
+
+    f32x16 acc[YB][XB];
+#pragma unroll
+    for (int m = 0; m < YB; ++m)
+#pragma unroll
+        for (int n = 0; n < XB; ++n)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.0f;
+
+    // ---- scales.  Of this wave's columns: one block ----
+    const int xblock = min((c0 + wx * WCOLS) / kBlock, (TRX ? KB : NB) - 1);
+    uint32_t ysc[YB][kScaleWords];
+    int xsc[PARTS];
+    const uint8_t* yscale[YB];
+#pragma unroll
+    for (int m = 0; m < YB; ++m) yscale[m] = g.y_scale + gather_row((wy + WY * m) * 32 + r32) * g.y_pitch;
+    // from stage `first` (a multiple of 4) on
+    auto load_scales = [&](int first) {
+        const int t = min(first + lane, nk - 1);
+        if constexpr (TRX) {
+            const bool second = t >= part_stages;
+            const uint8_t* p = second ? xscale[1] : xscale[0];
+            xsc[0] = p[static_cast<int64_t>(second ? t - part_stages : t) * KB + xblock];
+        } else {
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p) xsc[p] = xscale[p][static_cast<int64_t>(xblock) * KB + t];
+        }
+#pragma unroll
+        for (int i = 0; i < kScaleWords; ++i) {
+            if (first + 4 * i >= nk) continue;
+#pragma unroll
+            for (int m = 0; m < YB; ++m)
+                ysc[m][i] = *reinterpret_cast<const uint32_t*>(yscale[m] + first + 4 * i);
+        }
+    };
+
+    // the operand of rows [32 b, 32 b + 32) (along) or columns (down), substep ks
+    auto read_along = [&](uint32_t buf, int b, int ks) {
+        const int r = b * 32 + r32;
+        const unsigned char* row = s_arena + (buf - arena) + r * 128;
+        const int c = ks * 4 + half * 2, sw = (r >> 1) & 7;
+        const u32x4 lo = *reinterpret_cast<const u32x4*>(row + ((c ^ sw) << 4));
+        const u32x4 hi = *reinterpret_cast<const u32x4*>(row + (((c + 1) ^ sw) << 4));
+        return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+    };
+    auto read_down = [&](uint32_t buf, int b, int ks) {
+        const int i = lane & 15;
+        const int c = b * 2 + ((lane >> 4) & 1);
+        i32x8 v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = ks * 64 + half * 32 + j * 8 + (i >> 1);
+            const u32x2 t = lds_read_tr8(s_arena + (buf - arena) + r * BX + ((c ^ down_swizzle<BX>(r)) << 4) + (i & 1) * 8);
+            v[2 * j] = static_cast<int>(t[0]);
+            v[2 * j + 1] = static_cast<int>(t[1]);
+        }
+        return v;
+    };
+
+    // the stages, with NV valid row blocks in this wave
+    auto k_loop = [&](auto nv_tag) {
+        constexpr int NV = decltype(nv_tag)::value;
+        constexpr int NA = NV > 0 ? NV : 1;
+        constexpr int MF = NV * XB;  // matrix instructions per substep
+        struct Frags {
+            i32x8 y[NA];
+            i32x8 x[XB];
+        };
+        constexpr int NP = NV > 0 ? NV + XB : 0;
+        int ys[NA], xs[PARTS];
+        auto load_piece = [&](Frags& f, int yb, int xb, int ks, auto qc) {
+            constexpr int q = decltype(qc)::value;
+            if constexpr (q < NV) {
+                f.y[q] = read_along(y_buf(yb), wy + WY * q, ks);
+            } else if constexpr (NV > 0) {
+                constexpr int n = q - NV;
+                if constexpr (TRX)
+                    f.x[n] = read_down(x_buf(xb), wx * XB + n, ks);
+                else
+                    f.x[n] = read_along(x_buf(xb), wx * XB + n, ks);
+            }
+        };
+        auto load_frags = [&](Frags& f, int yb, int xb, int ks) {
+            static_for<0, NP>([&](auto qc) { load_piece(f, yb, xb, ks, qc); });
+        };
+        auto mfma_one = [&](const Frags& f, auto ic) {
+            constexpr int i = decltype(ic)::value;
+            if constexpr (NV > 0) {
+                constexpr int m = i % NV, n = i / NV;
+                constexpr int p = GATED && n >= XB / 2 ? 1 : 0;
+                acc[m][n] = mfma32_fp8(f.x[n], f.y[m], acc[m][n], xs[p], ys[m]);
+            }
+        };
+        const int last = s1 - 1;
+        static_for<0, XA>([&](auto sc) {
+            constexpr int st = decltype(sc)::value;
+            if constexpr (st < YA) {
+#pragma unroll
+                for (int j = 0; j < DMA_Y; ++j) dma_y(j, st, min(s0 + st, last));
+            }
+#pragma unroll
+            for (int j = 0; j < DMA_X; ++j) dma_x(j, st, min(s0 + st, last));
+        });
+        int held = s0 & ~3;  // the stage whose scales lie in the first place
+        int held_x = held;   // and that of lane 0's column scale
+        load_scales(held);
+        wait_vmcnt<YOUNGER>();
+        __syncthreads();
+        int ybuf = 0, xbuf = 0;
+        Frags f0, f1;
+        load_frags(f0, 0, 0, 0);
+        for (int kt = s0; kt < s1; ++kt) {
+            if (kt - held_x == 4 * kScaleWords) {
+                held = held_x = kt;
+                load_scales(kt);
+            } else if (kt - held == 4) {
+                held = kt;
+#pragma unroll
+                for (int m = 0; m < NA; ++m)
+#pragma unroll
+                    for (int i = 0; i + 1 < kScaleWords; ++i) ysc[m][i] = ysc[m][i + 1];
+            }
+            const int shift = 8 * (kt - held);
+#pragma unroll
+            for (int m = 0; m < NA; ++m) ys[m] = static_cast<int>(ysc[m][0] >> shift);
+#pragma unroll
+            for (int p = 0; p < (GATED ? 2 : 1); ++p) xs[p] = __builtin_amdgcn_readlane(xsc[p], kt - held_x);
+            // past the end: an idle buffer is filled again
+            const int ky = min(kt + YA, last);
+            const int kx = min(kt + XA, last);
+            const int ynext = ybuf == 0 ? YBUFS - 1 : ybuf - 1;  // the buffer freed last
+            const int xnext = xbuf == 0 ? XBUFS - 1 : xbuf - 1;
+            // The stage's loads are spread over the matrix instructions of its
+            // two substeps, the reads of the next substep's operands between
+            // them (scheduling fences keep them there).  The barrier sits
+            // before the last eighth of the second substep, so the first
+            // operands of the next stage are read while those run.
+            constexpr int LOADS = DMA_X + DMA_Y;
+            auto substep = [&](const Frags& f, auto sc, auto lo_c, auto hi_c, Frags& fn, auto kn_c) {
+                constexpr int sub = decltype(sc)::value;
+                constexpr int LO = decltype(lo_c)::value, HI = decltype(hi_c)::value;
+                constexpr int KN = decltype(kn_c)::value;
+                constexpr int NM = HI - LO;
+                // this substep's loads: [L0, L1) of the stage's
+                constexpr int L0 = sub >= 0 ? (sub * LOADS + 1) / 2 : 0;
+                constexpr int L1 = sub >= 0 ? ((sub + 1) * LOADS + 1) / 2 : 0;
+                constexpr int NL = L1 - L0;
+                constexpr int NPC = KN >= 0 ? NP : 0;
+                constexpr int IT0 = NM > NL ? NM : NL;
+                constexpr int IT = IT0 > 0 ? IT0 : 1;
+                static_for<0, IT>([&](auto ic) {
+                    constexpr int i = decltype(ic)::value;
+                    static_for<0, NPC>([&](auto qc) {
+                        constexpr int q = decltype(qc)::value;
+                        if constexpr (q * IT / (NPC > 0 ? NPC : 1) == i) load_piece(fn, ybuf, xbuf, KN, qc);
+                    });
+                    if constexpr (i < NM) mfma_one(f, std::integral_constant<int, LO + i>{});
+                    constexpr int step = NM >= NL ? (NL > 0 ? NM / NL : 1) : 1;
+                    if constexpr (NL > 0 && i % step == step - 1 && i / step < NL) {
+                        constexpr int j = L0 + i / step;
+                        if constexpr (j < DMA_Y)
+                            dma_y(j, ynext, ky);
+                        else
+                            dma_x(j - DMA_Y, xnext, kx);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                });
+            };
+            using C0 = std::integral_constant<int, 0>;
+            using CM = std::integral_constant<int, MF>;
+            using CH = std::integral_constant<int, MF * 7 / 8>;
+            using K0 = std::integral_constant<int, 0>;
+            using K1 = std::integral_constant<int, 1>;
+            using KNone = std::integral_constant<int, -1>;
+            substep(f0, K0{}, C0{}, CM{}, f1, K1{});
+            substep(f1, K1{}, C0{}, CH{}, f0, KNone{});
+            wait_vmcnt<YOUNGER>();
+            __syncthreads();
+            ybuf = ybuf == YBUFS - 1 ? 0 : ybuf + 1;
+            xbuf = xbuf == XBUFS - 1 ? 0 : xbuf + 1;
+            load_frags(f0, ybuf, xbuf, 0);  // after the last stage: read, never used
+            __builtin_amdgcn_sched_barrier(0);
+            substep(f1, KNone{}, CH{}, CM{}, f0, KNone{});
+        }
+        wait_vmcnt<0>();
+        __syncthreads();
+    };
+    static_for<0, YB + 1>([&](auto nv_tag) {
+        if (valid_blocks == decltype(nv_tag)::value) k_loop(nv_tag);
+    });
+
+    // ---- epilogue: through LDS, one block of 32 rows of this wave at a time
+    // (a region of its own), so that the stores are 16 bytes a lane over whole
+    // rows ----
+    constexpr int PITCH = WCOLS * 4 + 16;  // 4-byte elements; others: WCOLS * their bytes + 16
+    constexpr int REGION = 32 * PITCH;
+    static_assert(4 * REGION + BY * WX * 8 <= Shape::kArena, "epilogue region");
+    unsigned char* region = s_arena + wave * REGION;
+    const int wc0 = c0 + wx * WCOLS;
+    // 32 rows at `from` in LDS to rows of `width` elements of BYTES each, at
+    // column wc0, columns below `end`
+    auto put_rows = [&](auto bytes_c, const unsigned char* from, void* out, int64_t width, int blk, int end) {
+        constexpr int BYTES = decltype(bytes_c)::value;
+        constexpr int LPR = WCOLS * BYTES / 16;  // lanes per row
+        const int left = rows - blk * 32;        // rows of this block inside the tile
+#pragma unroll
+        for (int it = 0; it < 32 * LPR / 64; ++it) {
+            const int r = it * (64 / LPR) + lane / LPR, c = lane % LPR * (16 / BYTES);
+            const u32x4 v = ld16(from + r * (WCOLS * BYTES + 16) + c * BYTES);
+            if (r < left && wc0 + c < end)
+                *reinterpret_cast<u32x4*>(static_cast<unsigned char*>(out) +
+                                          ((orow0 + blk * 32 + r) * width + wc0 + c) * BYTES) = v;
+        }
+    };
+    using B1 = std::integral_constant<int, 1>;
+    using B2 = std::integral_constant<int, 2>;
+
+    if constexpr (!GATED) {
+        const bool out_bf16 = g.out_bf16 && !split, accumulate = g.accumulate && !split;
+        float* const out = split ? static_cast<float*>(g.ws) + static_cast<int64_t>(blockIdx.y) * g.P * cols
+                                 : static_cast<float*>(g.out);
+#pragma unroll
+        for (int m = 0; m < YB; ++m) {
+            if (m >= valid_blocks) continue;
+            const int blk = wy + WY * m;
+#pragma unroll
+            for (int n = 0; n < XB; ++n)
+#pragma unroll
+                for (int i4 = 0; i4 < 4; ++i4) {
+                    const int col = n * 32 + 8 * i4 + 4 * half;
+                    f32x4 v;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = acc[m][n][4 * i4 + i];
+                    if (out_bf16) {
+                        const u32x2 b = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+                        *reinterpret_cast<u32x2*>(region + r32 * (WCOLS * 2 + 16) + col * 2) = b;
+                    } else {
+                        *reinterpret_cast<f32x4*>(region + r32 * PITCH + col * 4) = v;
+                    }
+                }
+            wave_lds_fence();
+            if (out_bf16) {
+                put_rows(B2{}, region, g.out, cols, blk, cols);
+            } else {
+                constexpr int LPR = WCOLS / 4;
+                const int left = rows - blk * 32;
+#pragma unroll
+                for (int it = 0; it < 32 * LPR / 64; ++it) {
+                    const int r = it * (64 / LPR) + lane / LPR, c = lane % LPR * 4;
+                    f32x4 v = *reinterpret_cast<const f32x4*>(region + r * PITCH + c * 4);
+                    if (r < left && wc0 + c < cols) {
+                        f32x4* o = reinterpret_cast<f32x4*>(out + (orow0 + blk * 32 + r) * cols + wc0 + c);
+                        if (accumulate) v += *o;
+                        *o = v;
+                    }
+                }
+            }
+            wave_lds_fence();
+        }
+    } else {
+        // h = silu(g) u, or dg and du beside it; then the codes of the rows'
+        // blocks, whose largest magnitudes the waves of a row exchange
+        constexpr bool GRAD = MODE == kF8GateUpGrad;
+        constexpr int HB = XB / 2;
+        constexpr int CODES = 32 * (WCOLS * 2 + 16);  // the codes' place behind bf16 rows in the region
+        static_assert(!GRAD || CODES + 32 * (WCOLS + 16) <= REGION, "both fit");
+        uint32_t* const s_top = reinterpret_cast<uint32_t*>(s_arena + 4 * REGION);  // [2][BY][WX]
+        // h, dg and du of four places, from the accumulators and dh.  The
+        // gradients are computed in both passes below: kept, they would take
+        // the place of g and u and spill (256 registers each)
+        auto four = [&](int m, int n, int i4, f32x4& h, f32x4& dg, f32x4& du) {
+            f32x4 d = {0.f, 0.f, 0.f, 0.f};
+            if constexpr (GRAD) {
+                const int c = wc0 + n * 32 + 8 * i4 + 4 * half;
+                const int64_t q = orow0 + min((wy + WY * m) * 32 + r32, rows - 1);
+                if (c < cols) d = *reinterpret_cast<const f32x4*>(g.dh + q * cols + c);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = acc[m][n][4 * i4 + i], b = acc[m][n + HB][4 * i4 + i];
+                const float s = sigmoid_f32(a), silu = a * s;
+                h[i] = silu * b;
+                dg[i] = d[i] * b * (s + silu * (1.0f - s));
+                du[i] = d[i] * silu;
+            }
+        };
+#pragma unroll
+        for (int m = 0; m < YB; ++m) {
+            if (m >= valid_blocks) continue;
+            const int blk = wy + WY * m;
+            uint32_t top0 = 0, top1 = 0;
+#pragma unroll
+            for (int n = 0; n < HB; ++n)
+#pragma unroll
+                for (int i4 = 0; i4 < 4; ++i4) {
+                    f32x4 h, dg, du;
+                    four(m, n, i4, h, dg, du);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (GRAD) {
+                            top0 = max(top0, magnitude_bits(dg[i]));
+                            top1 = max(top1, magnitude_bits(du[i]));
+                        } else {
+                            top0 = max(top0, magnitude_bits(h[i]));
+                            acc[m][n][4 * i4 + i] = h[i];
+                        }
+                    }
+                    if constexpr (GRAD)
+                        *reinterpret_cast<u32x2*>(region + r32 * (WCOLS * 2 + 16) + (n * 32 + 8 * i4 + 4 * half) * 2) =
+                            u32x2{pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3])};
+                }
+            top0 = max(top0, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top0), 32, kWave)));
+            if constexpr (GRAD) top1 = max(top1, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top1), 32, kWave)));
+            if (half == 0) {
+                s_top[(blk * 32 + r32) * WX + wx] = top0;
+                if constexpr (GRAD) s_top[(BY + blk * 32 + r32) * WX + wx] = top1;
+            }
+            if constexpr (GRAD) {
+                wave_lds_fence();
+                put_rows(B2{}, region, g.h, cols, blk, cols);
+                wave_lds_fence();
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < YB; ++m) {
+            if (m >= valid_blocks) continue;
+            const int blk = wy + WY * m;
+#pragma unroll
+            for (int part = 0; part < (GRAD ? 2 : 1); ++part) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int w = 0; w < WX; ++w) top = max(top, s_top[(part * BY + blk * 32 + r32) * WX + w]);
+                const int scale = fp8_scale_of(top);
+                const float inverse = __uint_as_float(fp8_inverse_bits(scale));
+#pragma unroll
+                for (int n = 0; n < HB; ++n)
+#pragma unroll
+                    for (int i4 = 0; i4 < 4; ++i4) {
+                        const int col = n * 32 + 8 * i4 + 4 * half;
+                        f32x4 v;
+                        if constexpr (GRAD) {
+                            f32x4 h, dg, du;
+                            four(m, n, i4, h, dg, du);
+                            v = part ? du : dg;
+                            *reinterpret_cast<u32x2*>(region + r32 * (WCOLS * 2 + 16) + col * 2) =
+                                u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) v[i] = acc[m][n][4 * i4 + i];
+                        }
+                        *reinterpret_cast<uint32_t*>(region + (GRAD ? CODES : 0) + r32 * (WCOLS + 16) + col) =
+                            block_codes(v, top, inverse);
+                    }
+                wave_lds_fence();
+                if constexpr (GRAD) put_rows(B2{}, region, part ? g.du : g.dg, cols, blk, cols);
+                // [dg | du]: every column of the last block is written, zeros
+                // behind the last, since the two parts are one reduction
+                put_rows(B1{}, region + (GRAD ? CODES : 0), g.q + (part ? static_cast<int64_t>(col_tiles) * kBlock : 0),
+                         g.q_cols, blk, GRAD ? col_tiles * kBlock : cols);
+                wave_lds_fence();
+                const int r = blk * 32 + r32;
+                if (wx == 0 && half == 0 && r < rows)
+                    g.q_scale[(orow0 + r) * g.q_pitch + part * col_tiles + nt] = static_cast<uint8_t>(scale);
+            }
+        }
+    }
+}
+
+template <int MODE, int BX, int BY, bool NT = false>
+hipError_t launch_tiles(const Fp8Args& g, hipStream_t s, int splits = 1) {
+    constexpr bool kGated = MODE == kF8GateUp || MODE == kF8GateUpGrad;
+    const int64_t grid = tile_grid(g.P, g.E, MODE == kF8InputGrad ? g.K : g.N, kGated ? BX / 2 : BX, BY);
+    if (grid <= 0) return hipSuccess;
+    if (grid > kMaxWorkgroups) return hipErrorInvalidConfiguration;
+    const dim3 blocks(static_cast<unsigned>(grid), splits), threads(kThreads);
+    if constexpr (MODE != kF8InputGrad) {
+        if (g.pairs) {
+            fp8_tile_kernel<MODE, BX, BY, true, NT><<<blocks, threads, 0, s>>>(g);
+            return hipGetLastError();
+        }
+    }
+    fp8_tile_kernel<MODE, BX, BY, false, NT><<<blocks, threads, 0, s>>>(g);
+    return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace moe

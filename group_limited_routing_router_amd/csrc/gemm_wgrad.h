@@ -31,11 +31,12 @@
 #pragma once
 
 #include "gemm_tile.h"
+#include "tile_plan.h"
 
 namespace moe {
 namespace {
 
-constexpr int kNumCu = 256;
+
 
 template <int BX, int BY, bool GATHER>
 struct WgradShape {

@@ -65,6 +65,14 @@ EXPORTS = ("moe_workspace_bytes", "moe_route", "moe_permute", "moe_expert_ffn",
            "moe_grouped_gemm_wgrad", "moe_quantize_rows_int8", "moe_grouped_gemm_int8",
            "moe_int8_workspace_bytes", "moe_expert_ffn_int8", "moe_forward_int8",
            "moe_backward_workspace_bytes", "moe_expert_ffn_backward",
+           # experts in FP8 with a scale for each block of 128 (include/moe_fp8.h)
+           "moe_fp8_block_scales", "moe_quantize_rows_fp8_block",
+           "moe_quantize_weights_fp8_block", "moe_grouped_gemm_fp8_block",
+           "moe_grouped_gemm_fp8_block_dgrad", "moe_expert_gate_up_fp8_block",
+           "moe_fp8_block_workspace_bytes", "moe_expert_ffn_fp8_block", "moe_forward_fp8_block",
+           "moe_fp8_block_backward_workspace_bytes", "moe_expert_ffn_fp8_block_backward",
+           # the norm in front of the block (include/moe_norm.h)
+           "moe_norm", "moe_norm_workspace_bytes", "moe_norm_backward",
            # measurement kernels (include/moe_peak.h)
            "moe_peak_stream_read", "moe_peak_mfma_bf16", "moe_peak_mfma_bf16_flops",
            "moe_peak_mfma_stream", "moe_peak_mfma_stream_flops", "moe_peak_mfma_stream_bytes")
@@ -159,6 +167,33 @@ def load_library():
         lib.moe_expert_ffn_backward.argtypes = [prob, P, P, P, P, P, P, P, P, P, P, P, i32, i32, P,
                                                 size, P]
         lib.moe_expert_ffn_backward.restype = st
+        i64, f32 = ctypes.c_int64, ctypes.c_float
+        lib.moe_fp8_block_scales.argtypes = [ctypes.c_int32]
+        lib.moe_fp8_block_scales.restype = ctypes.c_int32
+        lib.moe_quantize_rows_fp8_block.argtypes = [i64, ctypes.c_int32, P, P, P, P]
+        lib.moe_quantize_weights_fp8_block.argtypes = [ctypes.c_int32] * 3 + [P] * 4
+        lib.moe_grouped_gemm_fp8_block.argtypes = [gemm] + [P] * 7 + [i32, P, size, P]
+        lib.moe_grouped_gemm_fp8_block_dgrad.argtypes = [gemm] + [P] * 6 + [i32, i32, P, size, P]
+        lib.moe_expert_gate_up_fp8_block.argtypes = [prob] + [P] * 11
+        lib.moe_fp8_block_workspace_bytes.argtypes = [prob]
+        lib.moe_fp8_block_workspace_bytes.restype = size
+        lib.moe_expert_ffn_fp8_block.argtypes = [prob] + [P] * 10 + [i32, P, size, P]
+        lib.moe_forward_fp8_block.argtypes = [prob] + [P] * 10 + [i32, P, P, P, P, size, P]
+        lib.moe_fp8_block_backward_workspace_bytes.argtypes = [prob]
+        lib.moe_fp8_block_backward_workspace_bytes.restype = size
+        lib.moe_expert_ffn_fp8_block_backward.argtypes = ([prob] + [P] * 11 + [i32, P, P, P, i32, i32, P,
+                                                                               size, P])
+        lib.moe_norm.argtypes = [i64, ctypes.c_int32, P, i32, P, P, f32, i32, P, i32, P, P]
+        lib.moe_norm_workspace_bytes.argtypes = [i64, ctypes.c_int32]
+        lib.moe_norm_workspace_bytes.restype = size
+        lib.moe_norm_backward.argtypes = [i64, ctypes.c_int32, P, i32, P, i32, P, P, i32, P, i32, P, P, i32,
+                                          P, size, P]
+        for name in ("moe_quantize_rows_fp8_block", "moe_quantize_weights_fp8_block",
+                     "moe_grouped_gemm_fp8_block", "moe_grouped_gemm_fp8_block_dgrad",
+                     "moe_expert_gate_up_fp8_block", "moe_expert_ffn_fp8_block",
+                     "moe_forward_fp8_block", "moe_expert_ffn_fp8_block_backward", "moe_norm",
+                     "moe_norm_backward"):
+            getattr(lib, name).restype = st
         lib.moe_peak_stream_read.argtypes = [P, ctypes.c_size_t, ctypes.c_int, P, ctypes.c_int, P]
         lib.moe_peak_stream_read.restype = st
         lib.moe_peak_mfma_bf16.argtypes = [ctypes.c_int64, ctypes.c_int, P, ctypes.c_int, P]
@@ -481,6 +516,224 @@ def moe_expert_ffn_backward(p, x, sorted_pairs, expert_offsets, w_gate, w_up, w_
         _arg(dx, "dx", _F32, P * p.H, dev, empty), _arg(dw_gate, "dw_gate", dw_gate.dtype, n, dev),
         _arg(dw_up, "dw_up", dw_gate.dtype, n, dev),
         _arg(dw_down, "dw_down", dw_gate.dtype, n, dev), _dtype_code(dw_gate),
+        1 if accumulate else 0, wp, wn, _on(stream, dev)))
+
+
+# ---- experts in FP8 with a scale for each block of 128 (include/moe_fp8.h) ----
+#
+# Codes are torch.float8_e4m3fn or, the same bytes, torch.uint8; scales (the
+# exponent of a power of two + 127) torch.uint8.
+
+_U8, _E4M3 = torch.uint8, torch.float8_e4m3fn
+
+
+def _codes(t, name, n, device, nullable=False):
+    if t is None or t.dtype is _U8:
+        return _arg(t, name, _U8, n, device, nullable)
+    return _arg(t, name, _E4M3, n, device, nullable)
+
+
+def _blocks(n):
+    return (n + 127) // 128
+
+
+def moe_fp8_block_scales(C) -> int:
+    """Bytes of a row's scales for C columns."""
+    return int(load_library().moe_fp8_block_scales(C))
+
+
+def _pitch(C):
+    return (_blocks(C) + 3) // 4 * 4
+
+
+def moe_quantize_rows_fp8_block(x, codes, scales, stream=None):
+    """The rows of x [rows,K] bf16 as e4m3 codes [rows,K] and scales
+    [rows,moe_fp8_block_scales(K)], one for each 128 columns."""
+    lib = _lib or load_library()
+    dev = torch.cuda.current_device()
+    if x.dim() != 2:
+        raise ValueError(f"x has {x.dim()} dimensions, needs 2")
+    rows, K = x.shape
+    _check(lib.moe_quantize_rows_fp8_block(
+        rows, K, _arg(x, "x", _BF16, 0, dev), _codes(codes, "codes", rows * K, dev),
+        _arg(scales, "scales", _U8, rows * _pitch(K), dev), _on(stream, dev)))
+
+
+def moe_quantize_weights_fp8_block(w, codes, scales, stream=None):
+    """The matrices w [E,N,K] bf16 as e4m3 codes [E,N,K] and scales
+    [E,ceil(N/128),ceil(K/128)], one for each 128 x 128."""
+    lib = _lib or load_library()
+    dev = torch.cuda.current_device()
+    if w.dim() != 3:
+        raise ValueError(f"w has {w.dim()} dimensions, needs 3")
+    E, N, K = w.shape
+    _check(lib.moe_quantize_weights_fp8_block(
+        E, N, K, _arg(w, "w", _BF16, 0, dev), _codes(codes, "codes", E * N * K, dev),
+        _arg(scales, "scales", _U8, E * _blocks(N) * _blocks(K), dev), _on(stream, dev)))
+
+
+def moe_grouped_gemm_fp8_block(g, a, a_scale, sorted_pairs, expert_offsets, w, w_scale, out,
+                               ws=None, stream=None):
+    """out [P,N] (fp32 or bf16) = a[row(q)] . w[e]^T on dequantised codes."""
+    lib = _lib or load_library()
+    dev = torch.cuda.current_device()
+    P, S, E, N, K = g.P, g.S, g.E, g.N, g.K
+    wp, wn = _ws_args(ws, dev)
+    _check(lib.moe_grouped_gemm_fp8_block(
+        g, _codes(a, "a", S * K, dev), _arg(a_scale, "a_scale", _U8, S * _pitch(K), dev),
+        _arg(sorted_pairs, "sorted_pairs", _I32, P, dev, True),
+        _arg(expert_offsets, "expert_offsets", _I32, E + 1, dev, E == 1),
+        _codes(w, "w", E * N * K, dev), _arg(w_scale, "w_scale", _U8, E * _blocks(N) * _blocks(K), dev),
+        _arg(out, "out", out.dtype, P * N, dev), _dtype_code(out), wp, wn, _on(stream, dev)))
+
+
+def moe_grouped_gemm_fp8_block_dgrad(g, dout, dout_scale, expert_offsets, w, w_scale, da, ws=None,
+                                     accumulate=False, stream=None):
+    """da [P,K] (fp32 or bf16) = dout[q] . w[e] on dequantised codes; da +=
+    with accumulate."""
+    lib = _lib or load_library()
+    dev = torch.cuda.current_device()
+    P, E, N, K = g.P, g.E, g.N, g.K
+    wp, wn = _ws_args(ws, dev)
+    _check(lib.moe_grouped_gemm_fp8_block_dgrad(
+        g, _codes(dout, "dout", P * N, dev), _arg(dout_scale, "dout_scale", _U8, P * _pitch(N), dev),
+        _arg(expert_offsets, "expert_offsets", _I32, E + 1, dev, E == 1),
+        _codes(w, "w", E * N * K, dev), _arg(w_scale, "w_scale", _U8, E * _blocks(N) * _blocks(K), dev),
+        _arg(da, "da", da.dtype, P * K, dev), _dtype_code(da), 1 if accumulate else 0, wp, wn,
+        _on(stream, dev)))
+
+
+def _fp8_matrix(p, dev, q, s, name):
+    n = p.E * p.I * p.H
+    return (_codes(q, "q_" + name, n, dev),
+            _arg(s, "s_" + name, _U8, p.E * _blocks(p.I) * _blocks(p.H), dev))
+
+
+def _fp8_dispatch(p, dev, sorted_pairs, expert_offsets):
+    dense = p.E == 1 and p.k == 1
+    return (_arg(sorted_pairs, "sorted_pairs", _I32, p.T * p.k, dev, dense),
+            _arg(expert_offsets, "expert_offsets", _I32, p.E + 1, dev, dense))
+
+
+def moe_expert_gate_up_fp8_block(p, x, x_scale, sorted_pairs, expert_offsets, q_gate, s_gate, q_up,
+                                 s_up, h, h_scale, stream=None):
+    """h = silu(x . gate^T) (x . up^T) by position, quantised by rows: codes
+    [T*k,I] and scales [T*k,moe_fp8_block_scales(I)], from x as codes [T,H] and
+    scales."""
+    lib = _lib or load_library()
+    dev = torch.cuda.current_device()
+    P = p.T * p.k
+    _check(lib.moe_expert_gate_up_fp8_block(
+        p, _codes(x, "x", p.T * p.H, dev), _arg(x_scale, "x_scale", _U8, p.T * _pitch(p.H), dev),
+        *_fp8_dispatch(p, dev, sorted_pairs, expert_offsets), *_fp8_matrix(p, dev, q_gate, s_gate, "gate"),
+        *_fp8_matrix(p, dev, q_up, s_up, "up"), _codes(h, "h", P * p.I, dev),
+        _arg(h_scale, "h_scale", _U8, P * _pitch(p.I), dev), _on(stream, dev)))
+
+
+def moe_fp8_block_workspace_bytes(p: MoEProblem) -> int:
+    return int(load_library().moe_fp8_block_workspace_bytes(p))
+
+
+def moe_expert_ffn_fp8_block(p, x, sorted_pairs, expert_offsets, q_gate, s_gate, q_up, s_up, q_down,
+                             s_down, y, ws, stream=None):
+    """The experts in FP8: y [T*k,H] (fp32 or bf16) in sorted order from x
+    [T,H] bf16."""
+    lib = _lib or load_library()
+    dev = torch.cuda.current_device()
+    wp, wn = _ws_args(ws, dev)
+    _check(lib.moe_expert_ffn_fp8_block(
+        p, _arg(x, "x", _BF16, p.T * p.H, dev), *_fp8_dispatch(p, dev, sorted_pairs, expert_offsets),
+        *_fp8_matrix(p, dev, q_gate, s_gate, "gate"), *_fp8_matrix(p, dev, q_up, s_up, "up"),
+        *_fp8_matrix(p, dev, q_down, s_down, "down"), _arg(y, "y", y.dtype, p.T * p.k * p.H, dev),
+        _dtype_code(y), wp, wn, _on(stream, dev)))
+
+
+def moe_forward_fp8_block(p, x, w_router, bias, q_gate, s_gate, q_up, s_up, q_down, s_down, out,
+                          topk_ids, topk_weights, y, ws, stream=None):
+    """moe_forward with the experts in FP8 by blocks."""
+    lib = _lib or load_library()
+    dev = torch.cuda.current_device()
+    P = p.T * p.k
+    wp, wn = _ws_args(ws, dev)
+    _check(lib.moe_forward_fp8_block(
+        p, _arg(x, "x", _BF16, p.T * p.H, dev), _arg(w_router, "w_router", _BF16, p.E * p.H, dev),
+        _arg(bias, "bias", _F32, p.E, dev, True), *_fp8_matrix(p, dev, q_gate, s_gate, "gate"),
+        *_fp8_matrix(p, dev, q_up, s_up, "up"), *_fp8_matrix(p, dev, q_down, s_down, "down"),
+        _arg(out, "out", out.dtype, p.T * p.H, dev), _dtype_code(out),
+        _arg(topk_ids, "topk_ids", _I32, P, dev, True),
+        _arg(topk_weights, "topk_weights", _F32, P, dev, True), _arg(y, "y", _F32, P * p.H, dev),
+        wp, wn, _on(stream, dev)))
+
+
+def moe_fp8_block_backward_workspace_bytes(p: MoEProblem) -> int:
+    return int(load_library().moe_fp8_block_backward_workspace_bytes(p))
+
+
+def moe_expert_ffn_fp8_block_backward(p, x, sorted_pairs, expert_offsets, q_gate, s_gate, q_up, s_up,
+                                      q_down, s_down, dy, dx, dw_gate, dw_up, dw_down, ws,
+                                      accumulate=False, stream=None):
+    """The gradients of moe_expert_ffn_fp8_block from dy [T*k,H] bf16: dx
+    [T*k,H] (fp32 or bf16), both in sorted order, and dw_gate, dw_up [E,I,H],
+    dw_down [E,H,I] (all fp32 or all bf16; += with accumulate)."""
+    lib = _lib or load_library()
+    dev = torch.cuda.current_device()
+    P, n, empty = p.T * p.k, p.E * p.I * p.H, p.T == 0
+    wp, wn = _ws_args(ws, dev)
+    dispatch = (None, None) if empty else _fp8_dispatch(p, dev, sorted_pairs, expert_offsets)
+    if empty:
+        dispatch = (None, _arg(expert_offsets, "expert_offsets", _I32, p.E + 1, dev, p.E == 1))
+    _check(lib.moe_expert_ffn_fp8_block_backward(
+        p, _arg(x, "x", _BF16, p.T * p.H, dev, empty), *dispatch,
+        *_fp8_matrix(p, dev, q_gate, s_gate, "gate"), *_fp8_matrix(p, dev, q_up, s_up, "up"),
+        *_fp8_matrix(p, dev, q_down, s_down, "down"), _arg(dy, "dy", _BF16, P * p.H, dev, empty),
+        None if dx is None and empty else _arg(dx, "dx", dx.dtype, P * p.H, dev),
+        DTYPE_F32 if dx is None and empty else _dtype_code(dx),
+        _arg(dw_gate, "dw_gate", dw_gate.dtype, n, dev), _arg(dw_up, "dw_up", dw_gate.dtype, n, dev),
+        _arg(dw_down, "dw_down", dw_gate.dtype, n, dev), _dtype_code(dw_gate),
+        1 if accumulate else 0, wp, wn, _on(stream, dev)))
+
+
+# ---- the norm in front of the block (include/moe_norm.h) ----
+
+
+def _rows_of(x, name):
+    if x.dim() != 2:
+        raise ValueError(f"{name} has {x.dim()} dimensions, needs 2")
+    return x.shape
+
+
+def moe_norm(x, weight, bias, eps, out, stats=None, center=False, stream=None):
+    """out = (x - mean) / sqrt(var + eps) weight + bias by rows of x [rows,H]
+    (fp32 or bf16); without center the mean is left out (RMS norm).  stats
+    [rows,2] fp32 takes mean and 1 / sqrt(var + eps) for moe_norm_backward."""
+    lib = _lib or load_library()
+    dev = torch.cuda.current_device()
+    rows, H = _rows_of(x, "x")
+    _check(lib.moe_norm(
+        rows, H, _arg(x, "x", x.dtype, 0, dev), _dtype_code(x), _arg(weight, "weight", _F32, H, dev),
+        _arg(bias, "bias", _F32, H, dev, True), eps, 1 if center else 0,
+        _arg(out, "out", out.dtype, rows * H, dev), _dtype_code(out),
+        _arg(stats, "stats", _F32, rows * 2, dev, True), _on(stream, dev)))
+
+
+def moe_norm_workspace_bytes(rows, H) -> int:
+    return int(load_library().moe_norm_workspace_bytes(rows, H))
+
+
+def moe_norm_backward(dy, x, weight, stats, dx, dweight, dbias, ws, center=False, accumulate=False,
+                      stream=None):
+    """The gradients of moe_norm from dy [rows,H] and what the forward call was
+    given and wrote: dx [rows,H], dweight [H] and dbias [H] (or None) fp32 (+=
+    with accumulate)."""
+    lib = _lib or load_library()
+    dev = torch.cuda.current_device()
+    rows, H = _rows_of(x, "x")
+    wp, wn = _ws_args(ws, dev)
+    _check(lib.moe_norm_backward(
+        rows, H, _arg(dy, "dy", dy.dtype, rows * H, dev), _dtype_code(dy), _arg(x, "x", x.dtype, 0, dev),
+        _dtype_code(x), _arg(weight, "weight", _F32, H, dev), _arg(stats, "stats", _F32, rows * 2, dev),
+        1 if center else 0, _arg(dx, "dx", dx.dtype, rows * H, dev), _dtype_code(dx),
+        _arg(dweight, "dweight", _F32, H, dev), _arg(dbias, "dbias", _F32, H, dev, True),
         1 if accumulate else 0, wp, wn, _on(stream, dev)))
 
 
