@@ -96,12 +96,27 @@ __device__ __forceinline__ uint32_t block_codes(const f32x4& v, uint32_t top, fl
 
 __device__ __forceinline__ uint32_t magnitude_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
+// gemm_tile.h's tiles, and 32 rows of gate and up: two buffers of 36 KB, so
+// that two workgroups share a compute unit and one's first loads and writing
+// run beside the other's stages (256 experts of 2 x 2560 x 5120, 4 rows each:
+// 1051 us, with four buffers and a compute unit to itself 1113).
+template <int BX, int BY>
+struct Fp8Shape {
+    static constexpr int kWavesY = BY >= 64 ? 2 : 1, kWavesX = kWaves / kWavesY;
+    static constexpr bool kSmall = BX == 256 && BY == 32;
+    static constexpr int kXBufs = BY >= 64 ? 3 : (kSmall ? 2 : 4), kYBufs = BY >= 64 || kSmall ? 2 : 4;
+    static constexpr int kXStage = BX * 128, kYStage = BY * 128;
+    static constexpr int kArena = kXBufs * kXStage + kYBufs * kYStage;
+    static_assert(kArena <= 163840, "LDS budget");
+    static constexpr int kPerCu = kArena <= 81920 ? 2 : 1;
+};
+
 // Words of a row's scales held in registers: 40 stages, K = 5120.
 constexpr int kScaleWords = 10;
 
 template <int MODE, int BX, int BY, bool GATHER, bool NT>
-__global__ __launch_bounds__(kThreads, (TileShape<BX, BY>::kPerCu)) void fp8_tile_kernel(Fp8Args g) {
-    typedef TileShape<BX, BY> Shape;
+__global__ __launch_bounds__(kThreads, (Fp8Shape<BX, BY>::kPerCu)) void fp8_tile_kernel(Fp8Args g) {
+    typedef Fp8Shape<BX, BY> Shape;
     constexpr bool TRX = MODE == kF8InputGrad;
     constexpr bool GATED = MODE == kF8GateUp || MODE == kF8GateUpGrad;
     constexpr int PARTS = MODE == kF8Product ? 1 : 2;    // weight matrices
@@ -113,12 +128,15 @@ __global__ __launch_bounds__(kThreads, (TileShape<BX, BY>::kPerCu)) void fp8_til
     static_assert(!GATED || (COLS == kBlock && XB % 2 == 0), "a tile is a block of h");
     constexpr int XS = Shape::kXStage, YS = Shape::kYStage;
     constexpr int XBUFS = Shape::kXBufs, YBUFS = Shape::kYBufs;
-    constexpr int XA = XBUFS - 1, YA = YBUFS - 1;        // stages the loads run ahead
+    // Stages the loads run ahead.  Both operands of a stage are in registers
+    // half way through it, so a barrier there (MID) frees an operand's buffer
+    // for the loads of the stage after the next where it has only two
+    constexpr bool MID = YBUFS == 2, X_LATE = XBUFS == 2;
+    constexpr int XA = X_LATE ? 2 : XBUFS - 1, YA = MID ? 2 : YBUFS - 1;
+    static_assert(XA == YA && (MID || !X_LATE), "the count of younger loads");
     constexpr int DMA_X = BX / 32, DMA_Y = BY / 32;      // 1 KB loads per wave and stage
-    // loads younger than those of the next stage, at a stage's end: each stage
-    // loads Y first, then X
-    constexpr int YOUNGER = YA == 1 ? DMA_X : (XA - 1) * (DMA_X + DMA_Y);
-    static_assert(YA == 1 ? XA >= 1 : XA == YA, "the count above");
+    // loads younger than those of the next stage, at a stage's end
+    constexpr int YOUNGER = (XA - 1) * (DMA_X + DMA_Y);
 
     __shared__ __attribute__((aligned(1024))) unsigned char s_arena[Shape::kArena];
     const uint32_t arena = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(s_arena));
@@ -154,13 +172,10 @@ __global__ __launch_bounds__(kThreads, (TileShape<BX, BY>::kPerCu)) void fp8_til
 
     // ---- loads (gemm_tile.h) ----
     const int64_t matrix = static_cast<int64_t>(e) * N * K + static_cast<int64_t>(c0) * (TRX ? 1 : K);
-    const uint8_t* xbase[PARTS];
-    const uint8_t* xscale[PARTS];
-#pragma unroll
-    for (int p = 0; p < PARTS; ++p) {
-        xbase[p] = g.w[p] + matrix;
-        xscale[p] = g.w_scale[p] + static_cast<int64_t>(e) * NB * KB;
-    }
+    const uint8_t* const xbase0 = uniform(g.w[0] + matrix);
+    const uint8_t* const xbase1 = PARTS > 1 ? uniform(g.w[1] + matrix) : xbase0;
+    const uint8_t* const xscale0 = g.w_scale[0] + static_cast<int64_t>(e) * NB * KB;
+    const uint8_t* const xscale1 = PARTS > 1 ? g.w_scale[1] + static_cast<int64_t>(e) * NB * KB : xscale0;
     const uint8_t* ybase = g.y + (GATHER ? 0 : orow0 * g.y_cols);
     uint32_t vx[DMA_X], vy[DMA_Y];
     auto along_row = [&](int j, int per_wave) { return wave * per_wave + j * 8 + (lane >> 3); };
@@ -171,9 +186,12 @@ __global__ __launch_bounds__(kThreads, (TileShape<BX, BY>::kPerCu)) void fp8_til
         const int64_t s = g.pairs[q] / g.k;
         return s < 0 ? 0 : (s >= g.S ? g.S - 1 : s);
     };
-    // gated: the matrix and column of a stage's row, wave by wave: gate, up
+    // gated: the matrix and column of a stage's row, wave by wave: gate, up.
+    // A wave loads of one matrix, or of both, half its loads each
     constexpr int HALF = BX / WX / 2;
-    auto x_part = [&](int j) { return GATED ? (wave * (BX / 4) + j * 8) / HALF % 2 : 0; };
+    static_assert(!GATED || HALF * 2 == BX / 4 || HALF == BX / 4, "rows of a wave's loads");
+    auto x_second = [&](int j) { return GATED && (HALF == BX / 4 ? (wave & 1) != 0 : j >= DMA_X / 2); };
+    const uint32_t xbytes = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(min(COLS, cols - c0) * K));
 #pragma unroll
     for (int j = 0; j < DMA_X; ++j) {
         if constexpr (TRX) {
@@ -214,14 +232,13 @@ __global__ __launch_bounds__(kThreads, (TileShape<BX, BY>::kPerCu)) void fp8_til
             const int kk = second ? kt - part_stages : kt;
             const int valid = min(kBlock, g.N - kk * kBlock);
             dma_load16<NT>(at,
-                           make_rsrc(uniform((second ? xbase[1] : xbase[0]) + static_cast<int64_t>(kk) * kBlock * K),
+                           make_rsrc(uniform((second ? xbase1 : xbase0) + static_cast<int64_t>(kk) * kBlock * K),
                                      __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(valid * K - c0))),
                            vx[j], 0);
         } else {
             const bool past = kt == nk - 1 && along_chunk(along_row(j, BX / 4)) >= tail;
-            const uint32_t bytes = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(min(COLS, cols - c0) * K));
-            const uint8_t* base = GATED && x_part(j) ? xbase[PARTS - 1] : xbase[0];
-            dma_load16<NT>(at, make_rsrc(uniform(base), bytes), past ? kNoRowOffset : vx[j], static_cast<uint32_t>(kt * 128));
+            dma_load16<NT>(at, make_rsrc(uniform(x_second(j) ? xbase1 : xbase0), xbytes), past ? kNoRowOffset : vx[j],
+                           static_cast<uint32_t>(kt * 128));
         }
     };
     auto dma_y = [&](int j, int buf, int kt) {
@@ -247,20 +264,21 @@ __global__ __launch_bounds__(kThreads, (TileShape<BX, BY>::kPerCu)) void fp8_til
     // ---- scales.  Of this wave's columns: one block ----
     const int xblock = min((c0 + wx * WCOLS) / kBlock, (TRX ? KB : NB) - 1);
     uint32_t ysc[YB][kScaleWords];
-    int xsc[PARTS];
+    int xsc0, xsc1 = 0;
     const uint8_t* yscale[YB];
-#pragma unroll
-    for (int m = 0; m < YB; ++m) yscale[m] = g.y_scale + gather_row((wy + WY * m) * 32 + r32) * g.y_pitch;
+    static_for<0, YB>([&](auto mc) {
+        constexpr int m = decltype(mc)::value;
+        yscale[m] = g.y_scale + gather_row((wy + WY * m) * 32 + r32) * g.y_pitch;
+    });
     // from stage `first` (a multiple of 4) on
     auto load_scales = [&](int first) {
         const int t = min(first + lane, nk - 1);
         if constexpr (TRX) {
             const bool second = t >= part_stages;
-            const uint8_t* p = second ? xscale[1] : xscale[0];
-            xsc[0] = p[static_cast<int64_t>(second ? t - part_stages : t) * KB + xblock];
+            xsc0 = (second ? xscale1 : xscale0)[static_cast<int64_t>(second ? t - part_stages : t) * KB + xblock];
         } else {
-#pragma unroll
-            for (int p = 0; p < PARTS; ++p) xsc[p] = xscale[p][static_cast<int64_t>(xblock) * KB + t];
+            xsc0 = xscale0[static_cast<int64_t>(xblock) * KB + t];
+            if constexpr (GATED) xsc1 = xscale1[static_cast<int64_t>(xblock) * KB + t];
         }
 #pragma unroll
         for (int i = 0; i < kScaleWords; ++i) {
@@ -304,7 +322,7 @@ __global__ __launch_bounds__(kThreads, (TileShape<BX, BY>::kPerCu)) void fp8_til
             i32x8 x[XB];
         };
         constexpr int NP = NV > 0 ? NV + XB : 0;
-        int ys[NA], xs[PARTS];
+        int ys[NA], xs0 = 0, xs1 = 0;
         auto load_piece = [&](Frags& f, int yb, int xb, int ks, auto qc) {
             constexpr int q = decltype(qc)::value;
             if constexpr (q < NV) {
@@ -324,19 +342,16 @@ __global__ __launch_bounds__(kThreads, (TileShape<BX, BY>::kPerCu)) void fp8_til
             constexpr int i = decltype(ic)::value;
             if constexpr (NV > 0) {
                 constexpr int m = i % NV, n = i / NV;
-                constexpr int p = GATED && n >= XB / 2 ? 1 : 0;
-                acc[m][n] = mfma32_fp8(f.x[n], f.y[m], acc[m][n], xs[p], ys[m]);
+                acc[m][n] = mfma32_fp8(f.x[n], f.y[m], acc[m][n], GATED && n >= XB / 2 ? xs1 : xs0, ys[m]);
             }
         };
         const int last = s1 - 1;
         static_for<0, XA>([&](auto sc) {
             constexpr int st = decltype(sc)::value;
-            if constexpr (st < YA) {
-#pragma unroll
-                for (int j = 0; j < DMA_Y; ++j) dma_y(j, st, min(s0 + st, last));
-            }
 #pragma unroll
             for (int j = 0; j < DMA_X; ++j) dma_x(j, st, min(s0 + st, last));
+#pragma unroll
+            for (int j = 0; j < DMA_Y; ++j) dma_y(j, st, min(s0 + st, last));
         });
         int held = s0 & ~3;  // the stage whose scales lie in the first place
         int held_x = held;   // and that of lane 0's column scale
@@ -360,28 +375,27 @@ __global__ __launch_bounds__(kThreads, (TileShape<BX, BY>::kPerCu)) void fp8_til
             const int shift = 8 * (kt - held);
 #pragma unroll
             for (int m = 0; m < NA; ++m) ys[m] = static_cast<int>(ysc[m][0] >> shift);
-#pragma unroll
-            for (int p = 0; p < (GATED ? 2 : 1); ++p) xs[p] = __builtin_amdgcn_readlane(xsc[p], kt - held_x);
+            xs0 = __builtin_amdgcn_readlane(xsc0, kt - held_x);
+            if constexpr (GATED) xs1 = __builtin_amdgcn_readlane(xsc1, kt - held_x);
             // past the end: an idle buffer is filled again
             const int ky = min(kt + YA, last);
             const int kx = min(kt + XA, last);
-            const int ynext = ybuf == 0 ? YBUFS - 1 : ybuf - 1;  // the buffer freed last
-            const int xnext = xbuf == 0 ? XBUFS - 1 : xbuf - 1;
+            const int xnext = X_LATE ? xbuf : (xbuf == 0 ? XBUFS - 1 : xbuf - 1);  // the buffer freed last
+            const int ynext = MID ? ybuf : (ybuf == 0 ? YBUFS - 1 : ybuf - 1);
             // The stage's loads are spread over the matrix instructions of its
             // two substeps, the reads of the next substep's operands between
             // them (scheduling fences keep them there).  The barrier sits
             // before the last eighth of the second substep, so the first
             // operands of the next stage are read while those run.
-            constexpr int LOADS = DMA_X + DMA_Y;
             auto substep = [&](const Frags& f, auto sc, auto lo_c, auto hi_c, Frags& fn, auto kn_c) {
                 constexpr int sub = decltype(sc)::value;
                 constexpr int LO = decltype(lo_c)::value, HI = decltype(hi_c)::value;
                 constexpr int KN = decltype(kn_c)::value;
                 constexpr int NM = HI - LO;
-                // this substep's loads: [L0, L1) of the stage's
-                constexpr int L0 = sub >= 0 ? (sub * LOADS + 1) / 2 : 0;
-                constexpr int L1 = sub >= 0 ? ((sub + 1) * LOADS + 1) / 2 : 0;
-                constexpr int NL = L1 - L0;
+                // this substep's loads, x's in the first of two unless its
+                // buffer is still read there
+                constexpr int NX = (X_LATE ? sub == 1 : sub == 0) ? DMA_X : 0;
+                constexpr int NL = NX + (sub == 1 ? DMA_Y : 0);
                 constexpr int NPC = KN >= 0 ? NP : 0;
                 constexpr int IT0 = NM > NL ? NM : NL;
                 constexpr int IT = IT0 > 0 ? IT0 : 1;
@@ -394,11 +408,10 @@ __global__ __launch_bounds__(kThreads, (TileShape<BX, BY>::kPerCu)) void fp8_til
                     if constexpr (i < NM) mfma_one(f, std::integral_constant<int, LO + i>{});
                     constexpr int step = NM >= NL ? (NL > 0 ? NM / NL : 1) : 1;
                     if constexpr (NL > 0 && i % step == step - 1 && i / step < NL) {
-                        constexpr int j = L0 + i / step;
-                        if constexpr (j < DMA_Y)
-                            dma_y(j, ynext, ky);
+                        if constexpr (i / step < NX)
+                            dma_x(i / step, xnext, kx);
                         else
-                            dma_x(j - DMA_Y, xnext, kx);
+                            dma_y(i / step - NX, ynext, ky);
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 });
@@ -410,6 +423,7 @@ __global__ __launch_bounds__(kThreads, (TileShape<BX, BY>::kPerCu)) void fp8_til
             using K1 = std::integral_constant<int, 1>;
             using KNone = std::integral_constant<int, -1>;
             substep(f0, K0{}, C0{}, CM{}, f1, K1{});
+            if constexpr (MID) __syncthreads();  // nobody reads this stage's y again
             substep(f1, K1{}, C0{}, CH{}, f0, KNone{});
             wait_vmcnt<YOUNGER>();
             __syncthreads();

@@ -5,7 +5,11 @@
 //   dweight = sum over rows of dy xh,  dbias = sum over rows of dy
 //
 // (the RMS form: mean = 0, and no mean(d)).  Both are bound by memory: a row is
-// read once, stays in registers and is written once.
+// read once, stays in registers and is written once.  Rows of 5120 in fp32:
+// 65536 to bf16 at 5.7 TB/s, the gradient of 8192 at 4.5 TB/s (a copy of 2 GiB
+// moves 4.9 TB/s, a fill 6.8).  A lane holds at most 16 values of a row and
+// long rows take workgroups of up to 16 waves: 64 values a lane of 4 waves took
+// 213 us for the gradient of 4096 x 16384 in bf16, this 87.
 #include <type_traits>
 
 #include "common.h"
@@ -15,8 +19,9 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / kWave;
+// Threads of a workgroup: LANES lanes a row, at least 256.
+template <int LANES>
+constexpr int kThreads = LANES > 256 ? LANES : 256;
 
 struct Eight {
     float v[8];
@@ -55,7 +60,7 @@ __device__ __forceinline__ void store8(void* p, int64_t i, bool f32, const Eight
 }
 
 // The sum over the LANES lanes of a row, the same in each: a wave, or the
-// workgroup through s (kWaves places that no earlier sum still reads).
+// workgroup through s (a place for each wave, that no earlier sum still reads).
 template <int LANES>
 __device__ __forceinline__ float row_sum(float v, float* s) {
 #pragma unroll
@@ -65,17 +70,17 @@ __device__ __forceinline__ float row_sum(float v, float* s) {
         __syncthreads();
         v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) v += s[w];
+        for (int w = 0; w < LANES / kWave; ++w) v += s[w];
     }
     return v;
 }
 
 // LANES lanes a row, CHUNKS times 8 values each.
 template <bool F32, int LANES, int CHUNKS>
-__global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a) {
-    __shared__ float s_sum[2][kWaves];
+__global__ __launch_bounds__(kThreads<LANES>) void norm_kernel(NormArgs a) {
+    __shared__ float s_sum[2][LANES / kWave];
     const int lane = threadIdx.x % LANES;
-    const int64_t r = folded_index() * (kThreads / LANES) + threadIdx.x / LANES;
+    const int64_t r = folded_index() * (kThreads<LANES> / LANES) + threadIdx.x / LANES;
     if (r >= a.rows) return;  // whole waves, or the whole workgroup of one row
     const int64_t at = r * a.H;
     Eight x[CHUNKS];
@@ -125,13 +130,15 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a) {
 }
 
 // Each group of LANES lanes takes rows r, r + groups, ... and keeps its sums of
-// dweight and dbias in registers; they go to ws, a row of 2 H for each group.
+// dweight and dbias in registers.  They go to ws, two rows of H for each
+// workgroup.
 template <bool X32, bool D32, int LANES, int CHUNKS>
-__global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormArgs a, int64_t groups) {
-    __shared__ float s_sum[2][2][kWaves];
+__global__ __launch_bounds__(kThreads<LANES>) void norm_backward_kernel(NormArgs a) {
+    constexpr int GROUPS = kThreads<LANES> / LANES;  // of a workgroup
+    __shared__ float s_sum[2][2][LANES / kWave];
     const int lane = threadIdx.x % LANES;
-    const int64_t group = static_cast<int64_t>(blockIdx.x) * (kThreads / LANES) + threadIdx.x / LANES;
-    if (group >= groups) return;
+    const int64_t group = static_cast<int64_t>(blockIdx.x) * GROUPS + threadIdx.x / LANES;
+    const int64_t groups = static_cast<int64_t>(gridDim.x) * GROUPS;
     Eight dw[CHUNKS], db[CHUNKS];
 #pragma unroll
     for (int j = 0; j < CHUNKS; ++j) dw[j] = db[j] = Eight{};
@@ -179,93 +186,119 @@ __global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormArgs a, int
             store8(a.out, at + c, a.out_f32, o);
         }
     }
+    if constexpr (GROUPS > 1) {  // the waves' sums added in order, in the first wave
+        __shared__ Eight s_part[2][GROUPS - 1][LANES * CHUNKS];
+        const int w = threadIdx.x / LANES;
+#pragma unroll
+        for (int j = 0; j < CHUNKS; ++j) {
+            if (w == 0) continue;
+            s_part[0][w - 1][j * LANES + lane] = dw[j];
+            s_part[1][w - 1][j * LANES + lane] = db[j];
+        }
+        __syncthreads();
+        if (w) return;
+#pragma unroll
+        for (int j = 0; j < CHUNKS; ++j)
+            for (int k = 0; k < GROUPS - 1; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    dw[j].v[i] += s_part[0][k][j * LANES + lane].v[i];
+                    db[j].v[i] += s_part[1][k][j * LANES + lane].v[i];
+                }
+    }
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * 2 * a.H;
 #pragma unroll
     for (int j = 0; j < CHUNKS; ++j) {
         const int c = (j * LANES + lane) * 8;
         if (c >= a.H) continue;
-        store8(a.ws, group * 2 * a.H + c, true, dw[j]);
-        if (a.dbias) store8(a.ws, (group * 2 + 1) * a.H + c, true, db[j]);
+        store8(a.ws, at + c, true, dw[j]);
+        if (a.dbias) store8(a.ws, at + a.H + c, true, db[j]);
     }
 }
 
-// dweight and dbias (blockIdx.y) from the groups' sums, in a fixed order: a
-// workgroup takes 64 columns, a wave a quarter of the groups.
-__global__ __launch_bounds__(kThreads) void norm_sums_kernel(NormArgs a, int64_t groups) {
-    __shared__ float s_part[kWaves][kWave];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = blockIdx.x * kWave + lane;
-    float sum = 0.0f;
+// dweight and dbias (blockIdx.y) from the workgroups' sums, in a fixed order:
+// 64 columns, 4 a thread, every 16th sum.
+__global__ __launch_bounds__(256) void norm_sums_kernel(NormArgs a, int parts) {
+    __shared__ f32x4 s_part[16][16];
+    const int quad = threadIdx.x & 15, part = threadIdx.x >> 4;
+    const int c = (blockIdx.x * 16 + quad) * 4;
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
     if (c < a.H) {
         const float* p = a.ws + static_cast<int64_t>(blockIdx.y) * a.H + c;
-        const int64_t first = groups * wave / kWaves, last = groups * (wave + 1) / kWaves;
 #pragma unroll 8
-        for (int64_t g = first; g < last; ++g) sum += p[g * 2 * a.H];
+        for (int64_t g = part; g < parts; g += 16) sum += *reinterpret_cast<const f32x4*>(p + g * 2 * a.H);
     }
-    s_part[wave][lane] = sum;
+    s_part[part][quad] = sum;
     __syncthreads();
-    if (wave || c >= a.H) return;
-    sum = 0.0f;
+    if (part || c >= a.H) return;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) sum += s_part[w][lane];
-    float* out = (blockIdx.y ? a.dbias : a.dweight) + c;
+    for (int i = 1; i < 16; ++i) sum += s_part[i][quad];
+    f32x4* out = reinterpret_cast<f32x4*>((blockIdx.y ? a.dbias : a.dweight) + c);
     *out = a.accumulate ? *out + sum : sum;
 }
 
-// Lanes a row and chunks a lane, by the row's length.
+// Lanes a row and chunks a lane, by the row's length: a wave, then workgroups
+// of more and more waves, so that a lane holds at most 16 values of a row.
 template <typename F>
 hipError_t by_length(int H, F&& f) {
-    if (H <= 512) return f(std::integral_constant<int, kWave>{}, std::integral_constant<int, 1>{});
-    if (H <= 2048) return f(std::integral_constant<int, kThreads>{}, std::integral_constant<int, 1>{});
-    if (H <= 6144) return f(std::integral_constant<int, kThreads>{}, std::integral_constant<int, 3>{});
-    return f(std::integral_constant<int, kThreads>{}, std::integral_constant<int, 8>{});
+    using std::integral_constant;
+    using One = integral_constant<int, 1>;
+    using Two = integral_constant<int, 2>;
+    if (H <= 512) return f(integral_constant<int, 64>{}, One{});
+    if (H <= 2048) return f(integral_constant<int, 256>{}, One{});
+    if (H <= 4096) return f(integral_constant<int, 512>{}, One{});
+    if (H <= 8192) return f(integral_constant<int, 512>{}, Two{});
+    return f(integral_constant<int, 1024>{}, Two{});
 }
 
-int lanes_of(int H) { return H <= 512 ? kWave : kThreads; }
-
-// Groups that share the rows of the gradient.
-int64_t groups_of(int64_t rows, int H) {
-    const int64_t most = 512 * (kThreads / lanes_of(H));
-    return rows < most ? rows : most;
+// Workgroups that share the rows of the gradient: as many as run at once, each
+// writing its sums once (65536 x 1280: 512 of them 231 us, 1024 168, 1792 172;
+// 8192 x 5120: 256 of them 121, 512 92, 768 110, 1024 118; 4096 x 16384: 256 of
+// them 87, 512 92).
+int parts_of(int64_t rows, int H) {
+    const int64_t most = H <= 512 ? 512 : H <= 2048 ? 1024 : H <= 8192 ? 512 : 256;
+    const int64_t want = H <= 512 ? (rows + 3) / 4 : rows;
+    return static_cast<int>(want < most ? want : most);
 }
 
 }  // namespace
 
 size_t norm_ws_bytes(int64_t rows, int H) {
-    return static_cast<size_t>(groups_of(rows, H)) * 2 * static_cast<size_t>(H) * sizeof(float);
+    return rows <= 0 ? 0 : static_cast<size_t>(parts_of(rows, H)) * 2 * static_cast<size_t>(H) * sizeof(float);
 }
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
     if (a.rows <= 0) return hipSuccess;
     return by_length(a.H, [&](auto lanes, auto chunks) {
-        constexpr int L = decltype(lanes)::value, C = decltype(chunks)::value;
-        const dim3 grid = folded_grid((a.rows + kThreads / L - 1) / (kThreads / L));
+        constexpr int L = decltype(lanes)::value, C = decltype(chunks)::value, T = kThreads<L>;
+        const dim3 grid = folded_grid((a.rows + T / L - 1) / (T / L), T);
         if (a.x_f32)
-            norm_kernel<true, L, C><<<grid, dim3(kThreads), 0, s>>>(a);
+            norm_kernel<true, L, C><<<grid, dim3(T), 0, s>>>(a);
         else
-            norm_kernel<false, L, C><<<grid, dim3(kThreads), 0, s>>>(a);
+            norm_kernel<false, L, C><<<grid, dim3(T), 0, s>>>(a);
         return hipGetLastError();
     });
 }
 
 hipError_t launch_norm_backward(const NormArgs& a, hipStream_t s) {
-    const int64_t groups = groups_of(a.rows, a.H);
-    if (a.rows > 0) {
+    const int parts = a.rows > 0 ? parts_of(a.rows, a.H) : 0;
+    if (parts) {
         const hipError_t e = by_length(a.H, [&](auto lanes, auto chunks) {
             constexpr int L = decltype(lanes)::value, C = decltype(chunks)::value;
-            const dim3 grid(static_cast<unsigned>((groups + kThreads / L - 1) / (kThreads / L)));
+            const dim3 grid(static_cast<unsigned>(parts)), threads(kThreads<L>);
             if (a.x_f32 && a.dy_f32)
-                norm_backward_kernel<true, true, L, C><<<grid, dim3(kThreads), 0, s>>>(a, groups);
+                norm_backward_kernel<true, true, L, C><<<grid, threads, 0, s>>>(a);
             else if (a.x_f32)
-                norm_backward_kernel<true, false, L, C><<<grid, dim3(kThreads), 0, s>>>(a, groups);
+                norm_backward_kernel<true, false, L, C><<<grid, threads, 0, s>>>(a);
             else if (a.dy_f32)
-                norm_backward_kernel<false, true, L, C><<<grid, dim3(kThreads), 0, s>>>(a, groups);
+                norm_backward_kernel<false, true, L, C><<<grid, threads, 0, s>>>(a);
             else
-                norm_backward_kernel<false, false, L, C><<<grid, dim3(kThreads), 0, s>>>(a, groups);
+                norm_backward_kernel<false, false, L, C><<<grid, threads, 0, s>>>(a);
             return hipGetLastError();
         });
         if (e != hipSuccess) return e;
     }
-    norm_sums_kernel<<<dim3((a.H + kWave - 1) / kWave, a.dbias ? 2 : 1), dim3(kThreads), 0, s>>>(a, groups);
+    norm_sums_kernel<<<dim3((a.H + 63) / 64, a.dbias ? 2 : 1), dim3(256), 0, s>>>(a, parts);
     return hipGetLastError();
 }
 

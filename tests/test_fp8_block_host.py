@@ -185,7 +185,7 @@ def test_norm(lib):
     assert norm(rows=0, x=None, w=None) == 0
 
     need = moe.moe_norm_workspace_bytes(4, 64)
-    assert need == 4 * 2 * 64 * 4 and moe.moe_norm_workspace_bytes(4, 12) == 0
+    assert need == 2 * 64 * 4 and moe.moe_norm_workspace_bytes(4, 12) == 0
 
     def back(rows=4, H=64, dy=good, dyd=0, x=good, xd=0, w=good, stats=good, dx=good + 16, dxd=0, dw=good, db=None,
              ws=good, n=need):
