@@ -22,8 +22,14 @@
 // towards zero to a multiple of 2^-13 of the largest's power of two, and sum
 // the groups in fp32.  On normal values the cut is 1.5e-5 of the result, on
 // equal signs 8e-5: 200 times below the operands' own rounding (2^-4), and
-// below that of a bf16 output (2^-8).  Products widened to bf16 would be summed in
-// fp32 throughout, at half the rate.
+// below that of a bf16 output (2^-8).  Operands widened to bf16 (WIDE, codes times
+// scale, exact) are summed in fp32 throughout, at half the rate.  gate_up does
+// that on few rows: what g and u are off moves codes of h by whole steps (one
+// row of 20480 x 5120, y after the down product: 2.5e-3 off the exact pass
+// instead of 1.6e-3, y's own rounding), and the weight stream hides it (one row
+// 54.6 -> 56.8 us, 256 experts of 4 rows 1053 -> 1061).  On more rows it would
+// not (64 rows 1287 -> 1507; one matrix of 2 x 2560 x 5120, 512 rows: 42 -> 66),
+// nor in the products (one row of 20480 x 5120: 26.6 -> 32).
 //
 // Three forms:
 //   kF8Product    x = w[e] rows along K
@@ -111,10 +117,21 @@ struct Fp8Shape {
     static constexpr int kPerCu = kArena <= 81920 ? 2 : 1;
 };
 
+// 8 codes times their scale as bf16, exactly: 4 significant bits, and the
+// exponents of scales from 2^-108 to 2^119 leave bf16's range to the values.
+__device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi, float scale) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+    return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
 // Words of a row's scales held in registers: 40 stages, K = 5120.
 constexpr int kScaleWords = 10;
 
-template <int MODE, int BX, int BY, bool GATHER, bool NT>
+template <int MODE, int BX, int BY, bool GATHER, bool NT, bool WIDE>
 __global__ __launch_bounds__(kThreads, (Fp8Shape<BX, BY>::kPerCu)) void fp8_tile_kernel(Fp8Args g) {
     typedef Fp8Shape<BX, BY> Shape;
     constexpr bool TRX = MODE == kF8InputGrad;
@@ -340,7 +357,16 @@ __global__ __launch_bounds__(kThreads, (Fp8Shape<BX, BY>::kPerCu)) void fp8_tile
         };
         auto mfma_one = [&](const Frags& f, auto ic) {
             constexpr int i = decltype(ic)::value;
-            if constexpr (NV > 0) {
+            if constexpr (NV > 0 && WIDE) {
+                constexpr int m = i % NV, n = i / NV;
+                const float x = __uint_as_float(static_cast<uint32_t>(GATED && n >= XB / 2 ? xs1 : xs0) << 23);
+                const float y = __uint_as_float(static_cast<uint32_t>(ys[m]) << 23);
+                f32x16 c = acc[m][n];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    c = mfma32(widen(f.x[n][2 * k], f.x[n][2 * k + 1], x), widen(f.y[m][2 * k], f.y[m][2 * k + 1], y), c);
+                acc[m][n] = c;
+            } else if constexpr (NV > 0) {
                 constexpr int m = i % NV, n = i / NV;
                 acc[m][n] = mfma32_fp8(f.x[n], f.y[m], acc[m][n], GATED && n >= XB / 2 ? xs1 : xs0, ys[m]);
             }
@@ -374,7 +400,7 @@ __global__ __launch_bounds__(kThreads, (Fp8Shape<BX, BY>::kPerCu)) void fp8_tile
             }
             const int shift = 8 * (kt - held);
 #pragma unroll
-            for (int m = 0; m < NA; ++m) ys[m] = static_cast<int>(ysc[m][0] >> shift);
+            for (int m = 0; m < NA; ++m) ys[m] = static_cast<int>(ysc[m][0] >> shift) & (WIDE ? 255 : -1);
             xs0 = __builtin_amdgcn_readlane(xsc0, kt - held_x);
             if constexpr (GATED) xs1 = __builtin_amdgcn_readlane(xsc1, kt - held_x);
             // past the end: an idle buffer is filled again
@@ -618,7 +644,7 @@ __global__ __launch_bounds__(kThreads, (Fp8Shape<BX, BY>::kPerCu)) void fp8_tile
     }
 }
 
-template <int MODE, int BX, int BY, bool NT = false>
+template <int MODE, int BX, int BY, bool NT = false, bool WIDE = false>
 hipError_t launch_tiles(const Fp8Args& g, hipStream_t s, int splits = 1) {
     constexpr bool kGated = MODE == kF8GateUp || MODE == kF8GateUpGrad;
     const int64_t grid = tile_grid(g.P, g.E, MODE == kF8InputGrad ? g.K : g.N, kGated ? BX / 2 : BX, BY);
@@ -627,11 +653,11 @@ hipError_t launch_tiles(const Fp8Args& g, hipStream_t s, int splits = 1) {
     const dim3 blocks(static_cast<unsigned>(grid), splits), threads(kThreads);
     if constexpr (MODE != kF8InputGrad) {
         if (g.pairs) {
-            fp8_tile_kernel<MODE, BX, BY, true, NT><<<blocks, threads, 0, s>>>(g);
+            fp8_tile_kernel<MODE, BX, BY, true, NT, WIDE><<<blocks, threads, 0, s>>>(g);
             return hipGetLastError();
         }
     }
-    fp8_tile_kernel<MODE, BX, BY, false, NT><<<blocks, threads, 0, s>>>(g);
+    fp8_tile_kernel<MODE, BX, BY, false, NT, WIDE><<<blocks, threads, 0, s>>>(g);
     return hipGetLastError();
 }
 
