@@ -545,13 +545,25 @@ __global__ __launch_bounds__(kThreads, (Fp8Shape<BX, BY>::kPerCu)) void fp8_tile
         // h, dg and du of four places, from the accumulators and dh.  The
         // gradients are computed in both passes below: kept, they would take
         // the place of g and u and spill (256 registers each)
+        f32x4 dh[GRAD ? YB : 1][HB][4];  // all asked for at once, held over both passes
+        if constexpr (GRAD) {
+#pragma unroll
+            for (int m = 0; m < YB; ++m) {
+                const int64_t q = orow0 + min((wy + WY * m) * 32 + r32, rows - 1);
+#pragma unroll
+                for (int n = 0; n < HB; ++n)
+#pragma unroll
+                    for (int i4 = 0; i4 < 4; ++i4) {
+                        const int c = wc0 + n * 32 + 8 * i4 + 4 * half;
+                        const f32x4 v = *reinterpret_cast<const f32x4*>(g.dh + q * cols + min(c, cols - 4));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) dh[m][n][i4][i] = c < cols ? v[i] : 0.0f;
+                    }
+            }
+        }
         auto four = [&](int m, int n, int i4, f32x4& h, f32x4& dg, f32x4& du) {
             f32x4 d = {0.f, 0.f, 0.f, 0.f};
-            if constexpr (GRAD) {
-                const int c = wc0 + n * 32 + 8 * i4 + 4 * half;
-                const int64_t q = orow0 + min((wy + WY * m) * 32 + r32, rows - 1);
-                if (c < cols) d = *reinterpret_cast<const f32x4*>(g.dh + q * cols + c);
-            }
+            if constexpr (GRAD) d = dh[m][n][i4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float a = acc[m][n][4 * i4 + i], b = acc[m][n + HB][4 * i4 + i];
