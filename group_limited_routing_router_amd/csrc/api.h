@@ -214,7 +214,14 @@ inline moe::GemmArgs gemm_args(const moe_gemm_problem& g) {
 }
 
 inline size_t gemm_ws_bytes(const moe_gemm_problem& g) {
-    const size_t n = moe::grouped_ws_bytes(gemm_args(g)), fp8 = moe::fp8_ws_bytes(g.P, g.E, g.N, g.K);
+    return moe::grouped_ws_bytes(gemm_args(g));
+}
+
+// Scratch of every call on g, those of moe_fp8.h too.  The calls of moe_gemm.h
+// ask only for their own part: some shapes split in FP8 alone (2191 rows by 8
+// experts, 13744 x 1216), and there they go without a workspace.
+inline size_t all_gemm_ws_bytes(const moe_gemm_problem& g) {
+    const size_t n = gemm_ws_bytes(g), fp8 = moe::fp8_ws_bytes(g.P, g.E, g.N, g.K);
     return n > fp8 ? n : fp8;
 }
 

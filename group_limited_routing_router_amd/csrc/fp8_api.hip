@@ -203,7 +203,7 @@ MOE_EXPORT moe_status moe_grouped_gemm_fp8_block(const moe_gemm_problem* g, cons
     MOE_TRY(check_ptr(w, "w"));
     MOE_TRY(check_ptr(w_scale, "w_scale"));
     MOE_TRY(check_ptr(out, "out"));
-    MOE_TRY(check_gemm_ws(*g, ws, ws_bytes));
+    MOE_TRY(check_ws_bytes(all_gemm_ws_bytes(*g), ws, ws_bytes));
     moe::Fp8Args x = fp8_args(*g, sorted_pairs, expert_offsets);
     set_rows(x, a, a_scale, g->K);
     x.w[0] = w;
@@ -229,7 +229,7 @@ MOE_EXPORT moe_status moe_grouped_gemm_fp8_block_dgrad(const moe_gemm_problem* g
     MOE_TRY(check_ptr(w, "w"));
     MOE_TRY(check_ptr(w_scale, "w_scale"));
     MOE_TRY(check_ptr(da, "da"));
-    MOE_TRY(check_gemm_ws(*g, ws, ws_bytes));
+    MOE_TRY(check_ws_bytes(all_gemm_ws_bytes(*g), ws, ws_bytes));
     moe::Fp8Args x = fp8_args(*g, nullptr, expert_offsets);
     set_rows(x, dout, dout_scale, g->N);
     x.w[0] = w;

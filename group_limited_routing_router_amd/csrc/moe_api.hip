@@ -358,7 +358,7 @@ MOE_EXPORT moe_status moe_forward_noalloc(const moe_problem* p, const moe_bf16* 
 MOE_EXPORT size_t moe_gemm_workspace_bytes(const moe_gemm_problem* g) {
     if (check_gemm(g, 8) != MOE_OK) return 0;
     ok();
-    return gemm_ws_bytes(*g);
+    return all_gemm_ws_bytes(*g);
 }
 
 MOE_EXPORT moe_status moe_grouped_gemm(const moe_gemm_problem* g, const moe_bf16* a,

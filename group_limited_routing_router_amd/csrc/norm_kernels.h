@@ -7,8 +7,8 @@
 
 namespace moe {
 
-// A row stays in registers: 8 chunks of 8 values for each of 256 threads.
-constexpr int kNormMaxH = 8 * 8 * 256;
+// A row stays in registers: 2 chunks of 8 values for each of 1024 threads.
+constexpr int kNormMaxH = 2 * 8 * 1024;
 
 struct NormArgs {
     int64_t rows;

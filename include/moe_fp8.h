@@ -22,6 +22,8 @@
  *            are padding.
  *   weights  [E,N,K]: a block is 128 x 128 of one matrix (less at its edges).
  *            Scales [E, ceil(N / 128), ceil(K / 128)].
+ * The quantisers write scale bytes 19 to 247.  Operands made otherwise may use 1
+ * to 254 (255 is no scale) with dequantised values below 2^127.
  *
  * Sums.  The matrix instructions add 8 products of one block at a time, each
  * cut towards zero to a multiple of 2^-13 of the power of two of the largest,

@@ -12,6 +12,7 @@
  * center = 0 (RMS norm): mean[t] is taken as 0.  center not 0 (layer norm): the
  * mean of the row; the squares are those of the differences, a second pass
  * over the row's registers, so a mean far above the spread costs no digits.
+ * Sums of squares are fp32: magnitudes from about 1e18 on overflow (r = 0).
  */
 #ifndef MOE_NORM_H
 #define MOE_NORM_H
@@ -41,8 +42,8 @@ size_t moe_norm_workspace_bytes(int64_t rows, int32_t H);
  *     dbias   = sum over rows of dy
  *   dy      [rows,H] fp32 or bf16 (dy_dtype)
  *   x, x_dtype, weight, center  as the forward call;  stats as it wrote them
- *   dx      [rows,H] fp32 or bf16 (dx_dtype); may be dy itself where the types
- *           are the same
+ *   dx      [rows,H] fp32 or bf16 (dx_dtype); may be dy or x itself where the
+ *           types are the same
  *   dweight [H] fp32;  dbias [H] fp32 or NULL
  *   accumulate  not 0: dweight += and dbias +=
  * The sums over rows are fp32 in a fixed order.  With no rows dweight and dbias
