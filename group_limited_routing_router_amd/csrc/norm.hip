@@ -6,7 +6,7 @@
 //
 // (the RMS form: mean = 0, and no mean(d)).  Both are bound by memory: a row is
 // read once, stays in registers and is written once.  Rows of 5120 in fp32:
-// 65536 to bf16 at 5.7 TB/s, the gradient of 8192 at 4.5 TB/s (a copy of 2 GiB
+// 65536 to bf16 at 5.6-6.0 TB/s, the gradient of 8192 at 4.8 TB/s (a copy of 2 GiB
 // moves 4.9 TB/s, a fill 6.8).  A lane holds at most 16 values of a row and
 // long rows take workgroups of up to 16 waves: 64 values a lane of 4 waves took
 // 213 us for the gradient of 4096 x 16384 in bf16, this 87.
