@@ -128,19 +128,6 @@ __device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi, float scale) {
     return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// 1 / (1 + exp(-z)) within 3 units of the last place: exp(-z) = 2^n 2^f with n
-// whole and log2(e) in two parts, then a reciprocal (1 unit).  The epilogue is one
-// wave to a SIMD deep in such chains; with expf and a division the whole backward
-// pass of 45956 rows by 22 experts, H 512, I 11072, takes 6717 us for 6400.
-// Past 104 exp(-z) is 0 or infinite, and the result 1 or 0.
-__device__ __forceinline__ float sigmoid_by_exp2(float z) {
-    const float c = __builtin_amdgcn_fmed3f(z, -104.0f, 104.0f);
-    const float n = __builtin_rintf(c * -1.44269502f);
-    float f = __builtin_fmaf(c, -1.44269502f, -n);
-    f = __builtin_fmaf(c, -1.92596303e-8f, f);
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_ldexpf(__builtin_amdgcn_exp2f(f), static_cast<int>(n)));
-}
-
 // Words of a row's scales held in registers: 40 stages, K = 5120.
 constexpr int kScaleWords = 10;
 
@@ -580,7 +567,7 @@ __global__ __launch_bounds__(kThreads, (Fp8Shape<BX, BY>::kPerCu)) void fp8_tile
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float a = acc[m][n][4 * i4 + i], b = acc[m][n + HB][4 * i4 + i];
-                const float s = sigmoid_by_exp2(a), silu = a * s;
+                const float s = sigmoid_f32(a), silu = a * s;
                 h[i] = silu * b;
                 dg[i] = d[i] * b * (s + silu * (1.0f - s));
                 du[i] = d[i] * silu;
