@@ -1,11 +1,11 @@
-"""The gradients of the FP8 experts on 256-row tiles, for every number of rows of
-an expert from 1 to 256: every count of row blocks of a wave, and blocks that end
-at every row."""
+"""The FP8 experts and their gradients on 128- and 256-row tiles, for every number
+of rows of an expert: every count of row blocks of a wave, and blocks that end at
+every row."""
 import numpy as np
 import pytest
 import torch
 
-import _fp8block as f8
+import test_gpu_fp8_limits as limits
 from _grouped import offsets_of
 from test_gpu_fp8_experts import NAMES, Experts, backward, reference_gradients, within
 
@@ -50,3 +50,33 @@ def test_dense_rows(moe, left):
     assert torch.equal(got[0], want[0]) and torch.isfinite(want[0]).all()
     for n in NAMES:
         assert torch.equal(got[1][n], want[1][n])
+
+
+def every_count(monkeypatch, most):
+    counts = np.random.default_rng(most).permutation(np.arange(1, most + 1))
+    monkeypatch.setattr(limits, "draw_counts", lambda gen, P, E: counts)
+    return int(counts.sum())
+
+
+@pytest.mark.parametrize("op", ["product", "input_grad"])
+@pytest.mark.parametrize("most,N,K", [(256, 1040, 1024), (128, 272, 256)])
+def test_products(moe, monkeypatch, op, most, N, K):
+    limits.test_tiles(moe, op, (every_count(monkeypatch, most), most, N, K))
+
+
+@pytest.mark.parametrize("most", [256, 128])
+def test_gated(moe, monkeypatch, most):
+    limits.test_gated_tiles(moe, every_count(monkeypatch, most), most, 256, 192)
+
+
+def test_every_count_of_rows_small(moe):
+    """As above on 128 rows."""
+    counts = np.random.default_rng(5).permutation(np.arange(1, 129))
+    c = Experts(int(counts.sum()), 1, 128, 128, 192, seed=5)
+    c.counts, c.offsets = counts, offsets_of(counts)
+    dx, dw = backward(moe, c)
+    torch.cuda.synchronize()
+    rdx, tx, rdw, tw = reference_gradients(c)
+    assert within(dx, rdx, tx, F32) <= 1.0
+    for n in NAMES:
+        assert within(dw[n], rdw[n], tw[n], F32) <= 1.0
