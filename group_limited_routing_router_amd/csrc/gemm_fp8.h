@@ -93,11 +93,12 @@ __device__ __forceinline__ uint32_t pack_fp8(float a, float b, float c, float d)
     return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true));
 }
 
-// Codes of four values in a block whose largest magnitude has the bits top.
+// Codes of four values in a block whose largest magnitude has the bits top
+// (without a branch: see the epilogue).
 __device__ __forceinline__ uint32_t block_codes(const f32x4& v, uint32_t top, float inverse) {
-    if (top >= kInfBits) return 0x7f7f7f7fu;
-    if (top < kTinyBits) return 0;
-    return pack_fp8(v[0] * inverse, v[1] * inverse, v[2] * inverse, v[3] * inverse);
+    const uint32_t keep = top - kTinyBits < kInfBits - kTinyBits ? 0xffffffffu : 0u;
+    const uint32_t bad = top >= kInfBits ? 0x7f7f7f7fu : 0u;
+    return (pack_fp8(v[0] * inverse, v[1] * inverse, v[2] * inverse, v[3] * inverse) & keep) | bad;
 }
 
 __device__ __forceinline__ uint32_t magnitude_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
@@ -164,17 +165,18 @@ __global__ __launch_bounds__(kThreads, (Fp8Shape<BX, BY>::kPerCu)) void fp8_tile
     const int cols = MODE == kF8InputGrad ? g.K : g.N;
     const int col_tiles = (cols + COLS - 1) / COLS;
 
-    int e, nt, row0, rows;
-    {
-        int32_t* s_off = reinterpret_cast<int32_t*>(s_arena);
-        int32_t* s_tstart = s_off + (kMaxE + 1);
-        if (!find_tile<BY, BY >= 64 ? 64 : 1, kBand>(g.offsets, g.P, g.E, col_tiles, s_off, s_tstart, e, nt, row0, rows)) return;
-        e = __builtin_amdgcn_readfirstlane(e);
-        nt = __builtin_amdgcn_readfirstlane(nt);
-        row0 = __builtin_amdgcn_readfirstlane(row0);
-        rows = __builtin_amdgcn_readfirstlane(rows);
-        __syncthreads();  // everyone is done with the schedule before the arena is reused
-    }
+    // Inlined, and in variables of their own, so that the tile is in scalar
+    // registers: as a call it came back through scratch, and every branch on it
+    // below was a lane mask
+    int found[4];
+    bool work;
+    [[clang::always_inline]] work = find_tile<BY, BY >= 64 ? 64 : 1, kBand>(
+        g.offsets, g.P, g.E, col_tiles, reinterpret_cast<int32_t*>(s_arena),
+        reinterpret_cast<int32_t*>(s_arena) + (kMaxE + 1), found[0], found[1], found[2], found[3]);
+    if (!work) return;
+    const int e = __builtin_amdgcn_readfirstlane(found[0]), nt = __builtin_amdgcn_readfirstlane(found[1]);
+    const int row0 = __builtin_amdgcn_readfirstlane(found[2]), rows = __builtin_amdgcn_readfirstlane(found[3]);
+    __syncthreads();  // everyone is done with the schedule before the arena is reused
     const int c0 = nt * COLS;
     const int64_t orow0 = row0;
     const int nblk = (rows + 31) >> 5;
@@ -468,25 +470,40 @@ __global__ __launch_bounds__(kThreads, (Fp8Shape<BX, BY>::kPerCu)) void fp8_tile
 
     // ---- epilogue: through LDS, one block of 32 rows of this wave at a time
     // (a region of its own), so that the stores are 16 bytes a lane over whole
-    // rows ----
+    // rows.  Nothing here runs under a lane mask: on the 256-row tiles nearly
+    // all 512 registers hold sums or dh, and the compiler has been seen to move
+    // such values inside the mask of a store and to lose those of the other
+    // lanes.  Stores past the tile's rows or columns go to an offset past their
+    // buffer's end instead, and loads from there give zeros ----
     constexpr int PITCH = WCOLS * 4 + 16;  // 4-byte elements; others: WCOLS * their bytes + 16
     constexpr int REGION = 32 * PITCH;
     static_assert(4 * REGION + BY * WX * 8 <= Shape::kArena, "epilogue region");
     unsigned char* region = s_arena + wave * REGION;
     const int wc0 = c0 + wx * WCOLS;
-    // 32 rows at `from` in LDS to rows of `width` elements of BYTES each, at
-    // column wc0, columns below `end`
-    auto put_rows = [&](auto bytes_c, const unsigned char* from, void* out, int64_t width, int blk, int end) {
+    // this tile's rows of an output of `width` bytes a row: at most 256 x 65536
+    // x 4 bytes, or 256 x 131072
+    auto tile_rows = [&](void* out, int64_t width) {
+        uint8_t* const first = static_cast<uint8_t*>(out) + orow0 * width;
+        return make_rsrc(uniform(first), __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(rows * width)));
+    };
+    // place of 16 bytes in them: row r of block blk, column c0 + c (in elements)
+    // of the columns below `end`
+    auto place = [&](int width, int blk, int r, int c0, int c, int end, int bytes) {
+        return static_cast<uint32_t>((blk * 32 + r) * width + (c0 + c) * bytes) | (c0 + c < end ? 0u : kNoRowOffset);
+    };
+    // 32 rows at `from` in LDS to those rows, `width` elements of BYTES each, at
+    // column col, columns below `end`
+    auto put_rows = [&](auto bytes_c, const unsigned char* from, __amdgpu_buffer_rsrc_t out, int width, int blk, int col,
+                        int end) {
         constexpr int BYTES = decltype(bytes_c)::value;
         constexpr int LPR = WCOLS * BYTES / 16;  // lanes per row
-        const int left = rows - blk * 32;        // rows of this block inside the tile
+        int l = lane;
+        asm volatile("" : "+v"(l));  // its places are computed here, not held over the loop in registers
 #pragma unroll
         for (int it = 0; it < 32 * LPR / 64; ++it) {
-            const int r = it * (64 / LPR) + lane / LPR, c = lane % LPR * (16 / BYTES);
+            const int r = it * (64 / LPR) + l / LPR, c = l % LPR * (16 / BYTES);
             const u32x4 v = ld16(from + r * (WCOLS * BYTES + 16) + c * BYTES);
-            if (r < left && wc0 + c < end)
-                *reinterpret_cast<u32x4*>(static_cast<unsigned char*>(out) +
-                                          ((orow0 + blk * 32 + r) * width + wc0 + c) * BYTES) = v;
+            __builtin_amdgcn_raw_buffer_store_b128(v, out, place(width * BYTES, blk, r, col, c, end, BYTES), 0, 0);
         }
     };
     using B1 = std::integral_constant<int, 1>;
@@ -494,8 +511,8 @@ __global__ __launch_bounds__(kThreads, (Fp8Shape<BX, BY>::kPerCu)) void fp8_tile
 
     if constexpr (!GATED) {
         const bool out_bf16 = g.out_bf16 && !split, accumulate = g.accumulate && !split;
-        float* const out = split ? static_cast<float*>(g.ws) + static_cast<int64_t>(blockIdx.y) * g.P * cols
-                                 : static_cast<float*>(g.out);
+        void* const out = split ? static_cast<float*>(g.ws) + static_cast<int64_t>(blockIdx.y) * g.P * cols : g.out;
+        const __amdgpu_buffer_rsrc_t rsrc_out = tile_rows(out, static_cast<int64_t>(cols) * (out_bf16 ? 2 : 4));
 #pragma unroll
         for (int m = 0; m < YB; ++m) {
             if (m >= valid_blocks) continue;
@@ -517,19 +534,17 @@ __global__ __launch_bounds__(kThreads, (Fp8Shape<BX, BY>::kPerCu)) void fp8_tile
                 }
             wave_lds_fence();
             if (out_bf16) {
-                put_rows(B2{}, region, g.out, cols, blk, cols);
+                put_rows(B2{}, region, rsrc_out, cols, blk, wc0, cols);
             } else {
                 constexpr int LPR = WCOLS / 4;
-                const int left = rows - blk * 32;
 #pragma unroll
                 for (int it = 0; it < 32 * LPR / 64; ++it) {
                     const int r = it * (64 / LPR) + lane / LPR, c = lane % LPR * 4;
                     f32x4 v = *reinterpret_cast<const f32x4*>(region + r * PITCH + c * 4);
-                    if (r < left && wc0 + c < cols) {
-                        f32x4* o = reinterpret_cast<f32x4*>(out + (orow0 + blk * 32 + r) * cols + wc0 + c);
-                        if (accumulate) v += *o;
-                        *o = v;
-                    }
+                    const uint32_t to = place(cols * 4, blk, r, wc0, c, cols, 4);
+                    if (accumulate)
+                        v += __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc_out, to, 0, 0));
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rsrc_out, to, 0, 0);
                 }
             }
             wave_lds_fence();
@@ -544,25 +559,24 @@ __global__ __launch_bounds__(kThreads, (Fp8Shape<BX, BY>::kPerCu)) void fp8_tile
         uint32_t* const s_top = reinterpret_cast<uint32_t*>(s_arena + 4 * REGION);  // [2][BY][WX]
         // h, dg and du of four places, from the accumulators and dh.  The
         // gradients are computed in both passes below: kept, they would take
-        // the place of g and u and spill (256 registers each).  Registers are at
-        // their end here: with a few more in use (a sigmoid by exp2 and a
-        // reciprocal, 3-7% faster) values of dh were moved inside the stores'
-        // lane mask and lost where a block's rows end
+        // the place of g and u and spill (256 registers each)
         f32x4 dh[GRAD ? YB : 1][HB][4];  // all asked for at once, held over both passes
+        __amdgpu_buffer_rsrc_t rsrc_h, rsrc_dg, rsrc_du;
+        const __amdgpu_buffer_rsrc_t rsrc_q = tile_rows(g.q, g.q_cols), rsrc_scale = tile_rows(g.q_scale, g.q_pitch);
         if constexpr (GRAD) {
+            rsrc_h = tile_rows(g.h, N * 2);
+            rsrc_dg = tile_rows(g.dg, N * 2);
+            rsrc_du = tile_rows(g.du, N * 2);
+            const __amdgpu_buffer_rsrc_t rsrc_dh = tile_rows(const_cast<float*>(g.dh), N * 4);
 #pragma unroll
-            for (int m = 0; m < YB; ++m) {
-                const int64_t q = orow0 + min((wy + WY * m) * 32 + r32, rows - 1);
+            for (int m = 0; m < YB; ++m)
 #pragma unroll
                 for (int n = 0; n < HB; ++n)
 #pragma unroll
-                    for (int i4 = 0; i4 < 4; ++i4) {
-                        const int c = wc0 + n * 32 + 8 * i4 + 4 * half;
-                        const f32x4 v = *reinterpret_cast<const f32x4*>(g.dh + q * cols + min(c, cols - 4));
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) dh[m][n][i4][i] = c < cols ? v[i] : 0.0f;
-                    }
-            }
+                    for (int i4 = 0; i4 < 4; ++i4)
+                        dh[m][n][i4] = __builtin_bit_cast(
+                            f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                       rsrc_dh, place(cols * 4, wy + WY * m, r32, wc0, n * 32 + 8 * i4 + 4 * half, cols, 4), 0, 0));
         }
         auto four = [&](int m, int n, int i4, f32x4& h, f32x4& dg, f32x4& du) {
             f32x4 d = {0.f, 0.f, 0.f, 0.f};
@@ -603,13 +617,12 @@ __global__ __launch_bounds__(kThreads, (Fp8Shape<BX, BY>::kPerCu)) void fp8_tile
                 }
             top0 = max(top0, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top0), 32, kWave)));
             if constexpr (GRAD) top1 = max(top1, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top1), 32, kWave)));
-            if (half == 0) {
-                s_top[(blk * 32 + r32) * WX + wx] = top0;
-                if constexpr (GRAD) s_top[(BY + blk * 32 + r32) * WX + wx] = top1;
-            }
+            // both halves hold the same and write it to the same place
+            s_top[(blk * 32 + r32) * WX + wx] = top0;
+            if constexpr (GRAD) s_top[(BY + blk * 32 + r32) * WX + wx] = top1;
             if constexpr (GRAD) {
                 wave_lds_fence();
-                put_rows(B2{}, region, g.h, cols, blk, cols);
+                put_rows(B2{}, region, rsrc_h, cols, blk, wc0, cols);
                 wave_lds_fence();
             }
         }
@@ -645,15 +658,18 @@ __global__ __launch_bounds__(kThreads, (Fp8Shape<BX, BY>::kPerCu)) void fp8_tile
                             block_codes(v, top, inverse);
                     }
                 wave_lds_fence();
-                if constexpr (GRAD) put_rows(B2{}, region, part ? g.du : g.dg, cols, blk, cols);
+                if constexpr (GRAD) put_rows(B2{}, region, part ? rsrc_du : rsrc_dg, cols, blk, wc0, cols);
                 // [dg | du]: every column of the last block is written, zeros
                 // behind the last, since the two parts are one reduction
-                put_rows(B1{}, region + (GRAD ? CODES : 0), g.q + (part ? static_cast<int64_t>(col_tiles) * kBlock : 0),
-                         g.q_cols, blk, GRAD ? col_tiles * kBlock : cols);
+                const int first = part * col_tiles * kBlock;
+                put_rows(B1{}, region + (GRAD ? CODES : 0), rsrc_q, static_cast<int>(g.q_cols), blk, first + wc0,
+                         first + (GRAD ? col_tiles * kBlock : cols));
                 wave_lds_fence();
-                const int r = blk * 32 + r32;
-                if (wx == 0 && half == 0 && r < rows)
-                    g.q_scale[(orow0 + r) * g.q_pitch + part * col_tiles + nt] = static_cast<uint8_t>(scale);
+                if (wx == 0)
+                    __builtin_amdgcn_raw_buffer_store_b8(
+                        static_cast<uint8_t>(scale), rsrc_scale,
+                        static_cast<uint32_t>((blk * 32 + r32) * g.q_pitch + part * col_tiles + nt) | (half ? kNoRowOffset : 0u),
+                        0, 0);
             }
         }
     }
