@@ -118,8 +118,10 @@ struct Fp8Shape {
     static constexpr int kPerCu = kArena <= 81920 ? 2 : 1;
 };
 
-// 8 codes times their scale as bf16, exactly: 4 significant bits, and the
-// exponents of scales from 2^-108 to 2^119 leave bf16's range to the values.
+// 8 codes times their scale as bf16, exactly: codes have 4 significant bits and
+// are multiples of 2^-9, so from scale 2^-124 on (byte 3) they are multiples of
+// bf16's smallest, 2^-133, which the matrix instruction takes as it is; values
+// below 2^128 are finite.
 __device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi, float scale) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
