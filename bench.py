@@ -60,7 +60,7 @@ TRAFFIC_FILE = os.path.join(ROOT, "profiles", "traffic.json")
 # the products by themselves and what runs on them are not part of the block's
 # forward pass and do not invalidate its stored traffic)
 OTHER_SOURCES = {"peak.hip", "grouped.hip", "gemm_tile.h", "gemm_wgrad.h", "swiglu.hip", "codes.h",
-                 "tile_plan.h", "fp8.hip", "fp8_gated.hip", "fp8_api.hip", "fp8_codes.h", "gemm_fp8.h",
+                 "tile_plan.h", "fp8.hip", "fp8_gated.hip", "fp8_api.hip", "fp8_codes.h", "fp8_plan.h", "gemm_fp8.h",
                  "norm.hip", "norm_api.hip", "norm_kernels.h"}
 KERNEL_SOURCES = sorted(
     os.path.join("group_limited_routing_router_amd", "csrc", f)

@@ -1,8 +1,8 @@
 // fp8.hip -- FP8 with a scale for each block of 128: quantisation of rows and
 // of weights, and the launches of the tiled products (gemm_fp8.h).
 #include "common.h"
+#include "fp8_plan.h"
 #include "gemm_fp8.h"
-#include "tile_plan.h"
 
 namespace moe {
 namespace {
@@ -112,21 +112,6 @@ __global__ __launch_bounds__(kThreads) void fp8_join_kernel(Fp8Args g, int cols,
         *o = v;
     }
 }
-
-// Parts of a long reduction on 32 rows keep at most 32 stages: 40 tiles of 160
-// stages (one row, 5120 x 20480, weights from HBM) 65, 40, 39, 29, 34 us in 1, 2,
-// 4, 8, 16 parts; as an input gradient 93, 55, 49, 36 in 1, 2, 4, 8.
-TilePlan long_parts(TilePlan p, int red) {
-    while (p.rows == 32 && p.splits > 1 && p.splits < 16 && blocks_of(red) >= 32 * p.splits) p.splits *= 2;
-    return p;
-}
-
-TilePlan product_plan(int64_t P, int E, int N, int K) { return long_parts(plan_tiles(P, E, N, K, K, 1), K); }
-
-// red: length of the sums (twice N, in whole blocks, for two matrices at once)
-TilePlan input_grad_plan(int64_t P, int E, int red, int K) { return long_parts(plan_tiles(P, E, K, red, K, 1), red); }
-
-int pair_red(int N) { return 2 * blocks_of(N) * kBlock; }
 
 size_t sums_bytes(int splits, int64_t P, int cols) {
     return splits > 1 ? static_cast<size_t>(splits) * static_cast<size_t>(P) * static_cast<size_t>(cols) * 4 : 0;
