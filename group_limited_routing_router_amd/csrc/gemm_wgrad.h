@@ -27,7 +27,7 @@
 // 8192 tokens, 256 experts of 2560 x 5120, bf16: 2.65 ms, 9.0 GB moved (6.7 of
 // them the output), the matrix units busy 31% of it, a fifth of the LDS cycles
 // lost to bank conflicts.  With accumulate a tile's values are read one load
-// at a time, each waited for: 128 tokens, 2.4 ms written and 9.9 ms added to.
+// at a time, each waited for: 128 tokens, 2.4 ms written and 9.5 ms added to.
 #pragma once
 
 #include "gemm_tile.h"
@@ -35,8 +35,6 @@
 
 namespace moe {
 namespace {
-
-
 
 template <int BX, int BY, bool GATHER>
 struct WgradShape {
@@ -512,16 +510,16 @@ __global__ __launch_bounds__(kThreads, (WgradShape<BX, BY, GATHER>::kPerCu)) voi
 #pragma unroll
             for (int it = 0; it < PER_UNIT; ++it) {
                 const int orow = (wy * YB + m) * 32 + it * (64 / CPR) + lane / CPR;
-                const bool in = orow < rows && ocol < cols;
-                const uint32_t off = static_cast<uint32_t>(orow * row_bytes + ocol * OB);
-                if constexpr (ACC) {
-                    if (in && t.nk > 0) {
-                        f32x4* o = reinterpret_cast<f32x4*>(static_cast<unsigned char*>(g.out) + at0 + off);
-                        *o = *o + __builtin_bit_cast(f32x4, v[u & 1][it]);
-                    }
-                } else {
-                    __builtin_amdgcn_raw_buffer_store_b128(v[u & 1][it], rsrc, in ? off : kNoRowOffset, 0, 0);
-                }
+                // outside the tile: an offset past the buffer, no lane mask (the
+                // sums around it fill the registers).  Added to, an expert
+                // without positions leaves its gradient unread and unwritten
+                const bool in = orow < rows && ocol < cols && (!ACC || t.nk > 0);
+                const uint32_t off = static_cast<uint32_t>(orow * row_bytes + ocol * OB) | (in ? 0u : kNoRowOffset);
+                u32x4 o = v[u & 1][it];
+                if constexpr (ACC)
+                    o = __builtin_bit_cast(u32x4, __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, 0)) +
+                                                      __builtin_bit_cast(f32x4, o));
+                __builtin_amdgcn_raw_buffer_store_b128(o, rsrc, off, 0, 0);
             }
         };
         // unit u + 1 goes into LDS while unit u comes back

@@ -1,6 +1,6 @@
-"""The compiled tiles of the FP8 products, as built in libmoe.so: no spilled
-registers, no scratch memory, and no lane mask behind the last matrix
-instruction.
+"""The compiled tiles of the FP8 products and of the weight gradient, as built in
+libmoe.so: no spilled registers, no scratch memory, and no lane mask behind the
+last matrix instruction.
 
 On the 256-row tiles nearly all 512 registers hold sums or the gradient of h. A
 value that the compiler moves inside a lane mask, because registers run out
@@ -17,6 +17,11 @@ from group_limited_routing_router_amd import moe
 
 LLVM = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "llvm", "bin")
 MAGIC = b"__CLANG_OFFLOAD_BUNDLE__"
+# and how many there are: products of three tiles, gathered or not, with and
+# without weights past the caches; input gradients, not gathered; the gated pass
+# as the products, twice; weight gradients of two tiles, gathered or not, bf16,
+# fp32 and added to
+KERNELS = {"fp8_tile_kernel": 10 + 5 + 2 * 10, "gemm_wgrad_kernel": 2 * 2 * 3}
 
 
 def code_objects():
@@ -42,7 +47,7 @@ def tiles(tmp_path_factory):
     d = tmp_path_factory.mktemp("code")
     got = {}
     for i, code in enumerate(code_objects()):
-        if b"fp8_tile_kernel" not in code:
+        if not any(k.encode() in code for k in KERNELS):
             continue
         path = d / f"{i}.co"
         path.write_bytes(code)
@@ -56,9 +61,9 @@ def tiles(tmp_path_factory):
                                str(path)], check=True, capture_output=True, text=True).stdout
         for part in re.split(r"\n(?=[0-9a-f]+ <)", text):
             m = re.match(r"[0-9a-f]+ <(\S+)>:\n", part)
-            if m and "fp8_tile_kernel" in m.group(1):
+            if m and any(k in m.group(1) for k in KERNELS):
                 got[m.group(1)] = numbers[m.group(1)], [x.split("//")[0].strip() for x in part.splitlines()[1:]]
-    assert len(got) >= 30, sorted(got)
+    assert all(sum(k in name for name in got) == n for k, n in KERNELS.items()), sorted(got)
     return got
 
 
