@@ -26,7 +26,7 @@
 // scale, exact) are summed in fp32 throughout, at half the rate.  gate_up does
 // that on few rows: what g and u are off moves codes of h by whole steps (one
 // row of 20480 x 5120, y after the down product: 2.5e-3 off the exact pass
-// instead of 1.6e-3, y's own rounding), and the weight stream hides it (one row
+// instead of 1.7e-3, y's own rounding), and the weight stream hides it (one row
 // 54.6 -> 56.8 us, 256 experts of 4 rows 1053 -> 1061).  On more rows it would
 // not (64 rows 1287 -> 1507; one matrix of 2 x 2560 x 5120, 512 rows: 42 -> 66),
 // nor in the products (one row of 20480 x 5120: 26.6 -> 32).

@@ -34,9 +34,11 @@
  * operands as bf16 instead, exactly, and sums in fp32 throughout, where the
  * positions are at most 24 for each expert that can have any (T k / min(E, T k)).
  * A token's g and u then differ in the last bits on either side of that, and
- * with them some codes of h by a step.  As bf16, units of 2^-9 of a block are held
- * from scale byte 3 on, and what the quantisers round up to 2^128 (bf16 from
- * 31/32 of it on) is infinite.
+ * with them some codes of h by a step.  As bf16, units of 2^-9 of a block are
+ * held from scale byte 3 on, and what the quantisers round up to 2^128 (bf16 from
+ * 31/32 of it on) is infinite.  Measured against the definition in 64 bits, in
+ * norm, with bf16 outputs: products 1.7e-3 off (their own rounding), y of the
+ * pass at most 2.1e-3, dx of the gradients at most 2.7e-3.
  *
  * Rows gathered by sorted_pairs may take at most 4 GiB less 1 MiB of codes
  * (else MOE_ERR_UNSUPPORTED).

@@ -53,8 +53,9 @@ typedef struct moe_gemm_problem {
 
 /* Bytes of scratch the calls below need in `ws` for problem g (0 if g is
  * invalid, or if none is needed: ws may then be NULL).  One workspace sized
- * by this function serves every call on g, those of moe_fp8.h too; what it holds before a call does
- * not matter.  Calls that overlap need one workspace each. */
+ * by this function serves every call on g, those of moe_fp8.h too; what it
+ * holds before a call does not matter.  Calls that overlap need one workspace
+ * each. */
 size_t moe_gemm_workspace_bytes(const moe_gemm_problem* g);
 
 /* The product: out[q,n] = sum_k a[row(q),k] * w[e,n,k], e the expert that
